@@ -28,7 +28,11 @@ EXPORTS = ("prism_query_sizes", "prism_zone_indicator", "prism_assign_shapes", "
            "prism_layer_backward", "prism_layer_step_host", "prism_layer_release", "prism_layer_sizeof",
            "prism_zone_partials", "prism_zone_finalize", "prism_block_pool_score_raster",
            "prism_sparse_attn_fwd_raster", "prism_sparse_attn_bwd_raster", "prism_attn_bwd_ds_bytes",
-           "prism_sparse_attn_bwd_ds", "prism_sparse_attn_bwd_raster_ds")
+           "prism_sparse_attn_bwd_ds", "prism_sparse_attn_bwd_raster_ds",
+           "prism_block_norm_ws_bytes", "prism_block_norm_fwd", "prism_block_norm_bwd",
+           "prism_head_rotate_ws_bytes", "prism_head_rotate_fwd", "prism_head_rotate_bwd",
+           "prism_expert_sizes", "prism_expert_plan", "prism_expert_dispatch", "prism_expert_combine",
+           "prism_expert_combine_bwd")
 GUIDANCE = {"joint": 0, "video": 1, "audio": 2}
 NOALLOC_SCRATCH_BYTES = 2 << 20
 
@@ -67,6 +71,30 @@ class LayerT(ctypes.Structure):
                 ("ws_bwd", _VP), ("ws_bwd_bytes", ctypes.c_size_t),
                 ("Q", _VP), ("K", _VP), ("V", _VP), ("hhat", _VP), ("O", _VP), ("dO", _VP),
                 ("dQ", _VP), ("dK", _VP), ("dV", _VP), ("io_events", _VP)]
+
+
+class BlockNormT(ctypes.Structure):
+    """Mirror of prism_block_norm_t."""
+    _fields_ = ([("rows", ctypes.c_int64), ("rows_per_group", ctypes.c_int64), ("channels", ctypes.c_int32),
+                 ("stream_dtype", ctypes.c_int32), ("branch_dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
+                 ("post_norm", ctypes.c_int32), ("eps", ctypes.c_float), ("res_scale", ctypes.c_float)]
+                + [("ld_" + n, ctypes.c_int64) for n in ("x", "h", "z", "y", "dx", "dh", "dz", "dy", "gate", "scale",
+                                                         "shift")])
+
+
+class RotateT(ctypes.Structure):
+    """Mirror of prism_rotate_t."""
+    _fields_ = ([("tokens", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("T", "H", "W", "heads_q", "heads_k", "head_dim", "pairs_t", "pairs_h",
+                                                 "pairs_w", "pairing", "dtype", "norm")]
+                + [("eps", ctypes.c_float)]
+                + [("ld_" + n, ctypes.c_int64) for n in ("q", "k", "qo", "ko", "dq", "dk")])
+
+
+class ExpertsT(ctypes.Structure):
+    """Mirror of prism_experts_t."""
+    _fields_ = [("rows", ctypes.c_int64), ("top_k", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("align", ctypes.c_int32), ("id_bytes", ctypes.c_int32)]
 
 
 class PrismError(RuntimeError):
@@ -117,6 +145,17 @@ _SIGS = {
     "prism_sparse_attn_bwd_raster_ds": [_PROB, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _P, _SZ,
                                         _P, _SZ, _P],
     "prism_zone_finalize": [_PROB, _P, _F, _I, _P, _P, _P, _P, _P, _SZ, _P],
+    "prism_block_norm_ws_bytes": [_P, _P],
+    "prism_block_norm_fwd": [_P] * 12,
+    "prism_block_norm_bwd": [_P] * 19 + [_SZ, _P],
+    "prism_head_rotate_ws_bytes": [_P, _P],
+    "prism_head_rotate_fwd": [_P] * 9,
+    "prism_head_rotate_bwd": [_P] * 13 + [_SZ, _P],
+    "prism_expert_sizes": [_P, _P, _P],
+    "prism_expert_plan": [_P] * 7 + [_SZ, _P],
+    "prism_expert_dispatch": [_P, _I, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, _I, _P, _P],
+    "prism_expert_combine": [_P, _I, ctypes.c_int64, _P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, _P],
+    "prism_expert_combine_bwd": [_P, _I, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, _P, _P, _I, _P, _P, _P],
     "prism_layer_init": [ctypes.POINTER(LayerT), _PROB],
     "prism_layer_arena_bytes": [ctypes.POINTER(LayerT), ctypes.POINTER(ctypes.c_size_t)],
     "prism_layer_bind": [ctypes.POINTER(LayerT), _P, _SZ],
@@ -370,3 +409,75 @@ def prism_sparse_attn_bwd_raster_ds(prob, Q, K, V, o_f32, dO, lse, perm, shape_i
         ctypes.byref(prob), _ptr(Q), _ptr(K), _ptr(V), _ptr(o_f32), _ptr(dO), _ptr(lse), _ptr(perm), _ptr(shape_id),
         _ptr(gsel), _ptr(gselT), scale, _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dev_status), _ptr(ws),
         ws.numel() * ws.element_size(), _ptr(ds), ds.numel() * ds.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the attention
+# Descriptors are passed by address (ctypes.addressof of a kept structure).
+def block_norm_ws_bytes(n: BlockNormT) -> int:
+    out = ctypes.c_size_t(0)
+    _check("prism_block_norm_ws_bytes", lib().prism_block_norm_ws_bytes(ctypes.addressof(n), ctypes.addressof(out)))
+    return out.value
+
+
+def prism_block_norm_fwd(n: BlockNormT, x, h, gate, w_post, w, b, scale, shift, z, y, stream=None):
+    _check("prism_block_norm_fwd", lib().prism_block_norm_fwd(
+        ctypes.addressof(n), _ptr(x), _ptr(h), _ptr(gate), _ptr(w_post), _ptr(w), _ptr(b), _ptr(scale), _ptr(shift),
+        _ptr(z), _ptr(y), _stream(stream)))
+
+
+def prism_block_norm_bwd(n: BlockNormT, z, h, gate, w_post, w, b, scale, dz, dy, dx, dh, dgate, dw_post, dw, db, dscale,
+                         dshift, ws, ws_bytes, stream=None):
+    _check("prism_block_norm_bwd", lib().prism_block_norm_bwd(
+        ctypes.addressof(n), _ptr(z), _ptr(h), _ptr(gate), _ptr(w_post), _ptr(w), _ptr(b), _ptr(scale), _ptr(dz),
+        _ptr(dy), _ptr(dx), _ptr(dh), _ptr(dgate), _ptr(dw_post), _ptr(dw), _ptr(db), _ptr(dscale), _ptr(dshift),
+        _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def head_rotate_ws_bytes(p: RotateT) -> int:
+    out = ctypes.c_size_t(0)
+    _check("prism_head_rotate_ws_bytes", lib().prism_head_rotate_ws_bytes(ctypes.addressof(p), ctypes.addressof(out)))
+    return out.value
+
+
+def prism_head_rotate_fwd(p: RotateT, Q, K, wq, wk, table, Qr, Kr, stream=None):
+    _check("prism_head_rotate_fwd", lib().prism_head_rotate_fwd(
+        ctypes.addressof(p), _ptr(Q), _ptr(K), _ptr(wq), _ptr(wk), _ptr(table), _ptr(Qr), _ptr(Kr), _stream(stream)))
+
+
+def prism_head_rotate_bwd(p: RotateT, Q, K, wq, wk, table, dQr, dKr, dQ, dK, dwq, dwk, ws, ws_bytes, stream=None):
+    _check("prism_head_rotate_bwd", lib().prism_head_rotate_bwd(
+        ctypes.addressof(p), _ptr(Q), _ptr(K), _ptr(wq), _ptr(wk), _ptr(table), _ptr(dQr), _ptr(dKr), _ptr(dQ), _ptr(dK),
+        _ptr(dwq), _ptr(dwk), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def expert_sizes(e: ExpertsT) -> tuple:
+    """(rows of a sorted buffer, workspace bytes of the plan)."""
+    rows, ws = ctypes.c_int64(0), ctypes.c_size_t(0)
+    _check("prism_expert_sizes", lib().prism_expert_sizes(ctypes.addressof(e), ctypes.addressof(rows),
+                                                          ctypes.addressof(ws)))
+    return rows.value, ws.value
+
+
+def prism_expert_plan(e: ExpertsT, ids, counts, offsets, pos, src, ws, ws_bytes, stream=None):
+    _check("prism_expert_plan", lib().prism_expert_plan(
+        ctypes.addressof(e), _ptr(ids), _ptr(counts), _ptr(offsets), _ptr(pos), _ptr(src), _ptr(ws), ws_bytes,
+        _stream(stream)))
+
+
+def prism_expert_dispatch(e: ExpertsT, dtype, channels, x, ld_x, pos, counts, offsets, clear_tail, xs, stream=None):
+    _check("prism_expert_dispatch", lib().prism_expert_dispatch(
+        ctypes.addressof(e), dtype, channels, _ptr(x), ld_x, _ptr(pos), _ptr(counts), _ptr(offsets), clear_tail, _ptr(xs),
+        _stream(stream)))
+
+
+def prism_expert_combine(e: ExpertsT, dtype, channels, y, pos, weights, add, ld_add, out, ld_out, stream=None):
+    _check("prism_expert_combine", lib().prism_expert_combine(
+        ctypes.addressof(e), dtype, channels, _ptr(y), _ptr(pos), _ptr(weights), _ptr(add), ld_add, _ptr(out), ld_out,
+        _stream(stream)))
+
+
+def prism_expert_combine_bwd(e: ExpertsT, dtype, channels, dout, ld_dout, y, pos, weights, counts, offsets, clear_tail,
+                             dy, dweights, stream=None):
+    _check("prism_expert_combine_bwd", lib().prism_expert_combine_bwd(
+        ctypes.addressof(e), dtype, channels, _ptr(dout), ld_dout, _ptr(y), _ptr(pos), _ptr(weights), _ptr(counts),
+        _ptr(offsets), clear_tail, _ptr(dy), _ptr(dweights), _stream(stream)))

@@ -271,10 +271,19 @@ class _PrismFn(torch.autograd.Function):
         return dQ, dK, dV, None, None
 
 
-def prism_attention(Q, K, V, hhat, mod: PrismSparseAttention):
+def prism_attention(Q, K, V, hhat, mod: PrismSparseAttention, rotation: dict | None = None):
     """Autograd entry: O = Prism sparse attention of raster Q, K, V guided by hhat.
 
     The selection statistics (rho, g, P) are constants for the backward, and
     hhat receives no gradient.
+
+    rotation: arguments of ``block.rotate`` (``table``, ``axes``, and as wanted
+    ``q_weight``, ``k_weight``, ``norm``, ``eps``, ``pairs``) for the norm and
+    the rotation of Q and K on the layer's grid, which the attention then reads;
+    the gradients go back through them.
     """
+    if rotation is not None:
+        from . import block
+        p = mod.prob
+        Q, K = block.rotate(Q, K, grid=(p.T, p.H, p.W), **rotation)
     return _PrismFn.apply(Q, K, V, hhat, mod)

@@ -480,6 +480,172 @@ prism_status_t prism_layer_release(prism_layer_t* L);
 /* sizeof(prism_layer_t) as compiled into the library (a check for bindings). */
 size_t prism_layer_sizeof(void);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around the attention: the rest of a transformer block's row operators
+ * ---------------------------------------------------------------------------
+ * The calls below take their own descriptors: any number of rows (tokens), 0
+ * included, and any width, not only the grids and heads of prism_problem_t.
+ * The conventions above hold (device pointers, caller-owned buffers,
+ * asynchronous on `stream`, errors before any launch).  Further:
+ *  - A row stride (ld_*) counts elements from one row to the next; 0 stands
+ *    for dense rows.  Channels are contiguous.  Block norms and experts take
+ *    pointers aligned to their elements, and any width and stride; what is not
+ *    on 16 bytes is moved by narrower accesses.  Workspaces and the rotation's
+ *    pointers and strides are on 16 bytes.
+ *  - All arithmetic is fp32; a bf16 result is rounded once, when stored.
+ *  - No call uses atomics on floating-point values: results do not depend on
+ *    scheduling.  A workspace may be reused as soon as the call's stream has
+ *    passed it; two calls that may overlap (two streams, two captured graphs)
+ *    need one each.
+ *  - No output may overlap an input or another output, except as stated.
+ */
+
+typedef enum { PRISM_NORM_NONE = 0, PRISM_NORM_RMS = 1, PRISM_NORM_LAYER = 2 } prism_norm_kind_t;
+
+/*
+ * Block norms — the norm before a block (attention or feed-forward), the norm
+ * after it, and the gated, scaled residual sum in between, in one pass:
+ *
+ *    z = res_scale x + gate_g * N_post(h) * w_post
+ *    y = N(z) * w * (1 + scale_g) + b * (1 + scale_g) + shift_g
+ *
+ * x is the residual stream before the block, h the block's output, z the
+ * stream after it and y the next block's input; row r uses row g = r /
+ * rows_per_group of gate, scale and shift (one row a sample, a frame, or a
+ * token).  N(v) = v / sqrt(mean v^2 + eps) (RMS), (v - mean) / sqrt(var + eps)
+ * (LAYER), or v (post_norm = NONE); statistics over the C channels.  y is
+ * formed from the unrounded z.
+ * Forms: h = NULL is the norm before the first block: z is x itself and is
+ * not written (z = NULL, res_scale unused).  norm = NONE ends with z (y =
+ * NULL, and w, b, scale, shift NULL).  Every vector may be NULL: gate, w,
+ * w_post count as 1, scale, shift, b as 0.
+ */
+typedef struct {
+    int64_t rows;            /* R >= 0                                            */
+    int64_t rows_per_group;  /* >= 1; the last group may be shorter               */
+    int32_t channels;        /* C, 1 .. 8192                                      */
+    int32_t stream_dtype;    /* of x, z, dz, dx                                   */
+    int32_t branch_dtype;    /* of h, y, dh, dy: stream_dtype, or bf16 with an
+                                f32 stream                                        */
+    int32_t norm;            /* prism_norm_kind_t of N                            */
+    int32_t post_norm;       /* prism_norm_kind_t of N_post                       */
+    float eps;               /* > 0, of both                                      */
+    float res_scale;
+    int64_t ld_x, ld_h, ld_z, ld_y;              /* row strides, 0 = C            */
+    int64_t ld_dx, ld_dh, ld_dz, ld_dy;
+    int64_t ld_gate, ld_scale, ld_shift;         /* between groups, 0 = C         */
+} prism_block_norm_t;
+
+/* Forward.  Vectors are float32: gate, scale, shift [groups][C], w_post, w, b
+ * [C].  z may be x itself (same pointer and stride). */
+prism_status_t prism_block_norm_fwd(const prism_block_norm_t* n, const void* x, const void* h,
+                                    const float* gate, const float* w_post, const float* w,
+                                    const float* b, const float* scale, const float* shift,
+                                    void* z, void* y, cudaStream_t stream);
+/*
+ * Backward.  z: the stored stream (x where h is NULL); h: the branch as the
+ * forward read it; dz (nullable: 0): the gradient that reaches z past this
+ * norm; dy (NULL where norm = NONE): of y.  Statistics are taken again from z
+ * and h.  Outputs: dx and dh (where there is h), and those wanted of dgate,
+ * dscale, dshift [groups][C] dense and dw_post, dw, db [C], float32 sums over
+ * the rows that share the vector.  A gradient needs its vector (dshift does
+ * not).  dx may be dz itself, dh may be h itself (same pointer and stride).
+ * ws: >= prism_block_norm_ws_bytes (nullable where none of the vectors'
+ * gradients is wanted).  With rows = 0 the [C] gradients are set to 0.
+ */
+prism_status_t prism_block_norm_ws_bytes(const prism_block_norm_t* n, size_t* bytes);
+prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, const void* z, const void* h,
+                                    const float* gate, const float* w_post, const float* w,
+                                    const float* b, const float* scale, const void* dz, const void* dy,
+                                    void* dx, void* dh, float* dgate, float* dw_post, float* dw,
+                                    float* db, float* dscale, float* dshift, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream);
+
+/*
+ * Head norm and rotation — Q and K of the attention, raster [tokens][heads][d]:
+ * an optional RMS norm of each head's d channels with weights, then the
+ * rotation of the head's d/2 channel pairs by angles that depend on the
+ * token's place (t, h, w) in the T x H x W grid.  Token i has place i mod
+ * (T H W), in raster order.  The first pairs_t pairs turn with t, the next
+ * pairs_h with h, the next pairs_w with w; the rest do not turn.
+ *    table: float32 (cos, sin) pairs, [T][pairs_t], then [H][pairs_h], then
+ *           [W][pairs_w] (positions and frequencies are the caller's)
+ *    pairs: INTERLEAVED channels (2i, 2i+1), HALF channels (i, i + d/2)
+ * One of heads_q, heads_k may be 0 (its pointers NULL); they may differ.
+ */
+typedef enum { PRISM_PAIRS_INTERLEAVED = 0, PRISM_PAIRS_HALF = 1 } prism_pairing_t;
+typedef struct {
+    int64_t tokens;                       /* >= 0                                 */
+    int32_t T, H, W;                      /* >= 1, any                            */
+    int32_t heads_q, heads_k, head_dim;   /* 0 .. 1024 each; 64 or 128            */
+    int32_t pairs_t, pairs_h, pairs_w;    /* sum <= head_dim / 2                  */
+    int32_t pairing, dtype, norm;         /* norm: 1 with the RMS norm, 0 without */
+    float eps;                            /* > 0                                  */
+    int64_t ld_q, ld_k, ld_qo, ld_ko, ld_dq, ld_dk;   /* elements between tokens
+                                             of Q, K, of the outputs and of dQr,
+                                             dKr; 0 = heads * head_dim; multiples
+                                             of 16 bytes                          */
+} prism_rotate_t;
+/* wq, wk: float32 [d] (nullable: 1; NULL without norm).  Qr may be Q itself and Kr K itself (same stride). */
+prism_status_t prism_head_rotate_fwd(const prism_rotate_t* p, const void* Q, const void* K,
+                                     const float* wq, const float* wk, const float* table, void* Qr,
+                                     void* Kr, cudaStream_t stream);
+/* Q, K as the forward read them (may be NULL without norm); dQ may be dQr itself, dK dKr itself.
+ * dwq, dwk float32 [d], nullable; ws >= prism_head_rotate_ws_bytes where one is wanted. */
+prism_status_t prism_head_rotate_ws_bytes(const prism_rotate_t* p, size_t* bytes);
+prism_status_t prism_head_rotate_bwd(const prism_rotate_t* p, const void* Q, const void* K,
+                                     const float* wq, const float* wk, const float* table,
+                                     const void* dQr, const void* dKr, void* dQ, void* dK, float* dwq,
+                                     float* dwk, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Experts — tokens sorted by expert and back.  Token t has top_k choices; slot
+ * i = t * top_k + j is its j-th, with expert ids[i].  An id outside [0,
+ * experts) drops the slot (padding tokens, capacity).  The sorted layout holds
+ * each expert's slots in ascending i from row offsets[e] on, offsets[e+1] =
+ * offsets[e] + counts[e] rounded up to a multiple of `align` (the row tile of
+ * the experts' products).  The number of sorted rows stays on the device; a
+ * sorted buffer holds rows_sorted rows (prism_expert_sizes, host only).
+ */
+typedef struct {
+    int64_t rows;            /* tokens, >= 0; rows * top_k <= 2^30                */
+    int32_t top_k;           /* 1 .. 16                                           */
+    int32_t experts;         /* 1 .. 1024                                         */
+    int32_t align;           /* 1 .. 4096                                         */
+    int32_t id_bytes;        /* 4 or 8: int32 or int64 ids                        */
+} prism_experts_t;
+prism_status_t prism_expert_sizes(const prism_experts_t* e, int64_t* rows_sorted, size_t* ws_bytes);
+/* ids [rows][top_k].  Outputs int32: counts [experts], offsets [experts + 1], pos [rows][top_k] (sorted
+ * row of each slot, -1: dropped), src [rows_sorted] (slot of each sorted row, -1: none). */
+prism_status_t prism_expert_plan(const prism_experts_t* e, const void* ids, int32_t* counts,
+                                 int32_t* offsets, int32_t* pos, int32_t* src, void* ws,
+                                 size_t ws_bytes, cudaStream_t stream);
+/*
+ * The moves, in dtype; sorted buffers (xs, y, dy) are dense [rows_sorted][channels], channels <= 2^20.
+ *   dispatch     xs[pos[i]] = x[t]: bit copies
+ *   combine      out[t] = add[t] + sum_j w[i] y[pos[i]] over the choices that are not dropped, j ascending
+ *                (weights float32 [rows][top_k], nullable: 1; add nullable: 0; a dropped slot's weight is not
+ *                read).  Without weights it is the gradient of dispatch.  out may be add itself.
+ *   combine_bwd  dy[pos[i]] = w[i] dout[t], dweights[i] = y[pos[i]] . dout[t] (nullable; 0 where dropped; y
+ *                may be NULL without it).  dy may be y itself.
+ * Rows between an expert's last slot and its next multiple of align are written 0 by dispatch and combine_bwd
+ * (of xs and dy).  Rows from offsets[experts] on are left as they were, or written 0 with clear_tail = 1.
+ */
+prism_status_t prism_expert_dispatch(const prism_experts_t* e, int32_t dtype, int64_t channels,
+                                     const void* x, int64_t ld_x, const int32_t* pos,
+                                     const int32_t* counts, const int32_t* offsets, int32_t clear_tail,
+                                     void* xs, cudaStream_t stream);
+prism_status_t prism_expert_combine(const prism_experts_t* e, int32_t dtype, int64_t channels,
+                                    const void* y, const int32_t* pos, const float* weights,
+                                    const void* add, int64_t ld_add, void* out, int64_t ld_out,
+                                    cudaStream_t stream);
+prism_status_t prism_expert_combine_bwd(const prism_experts_t* e, int32_t dtype, int64_t channels,
+                                        const void* dout, int64_t ld_dout, const void* y,
+                                        const int32_t* pos, const float* weights, const int32_t* counts,
+                                        const int32_t* offsets, int32_t clear_tail, void* dy,
+                                        float* dweights, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
