@@ -16,11 +16,13 @@ gradient accumulators that may belong to another stream.  Capture the explicit c
 Every step runs in ``libprism.so`` (contracts in ``include/prism.h``), on the current stream of the
 tensors' device.  Checks of shapes, types and devices raise ``ValueError``; what the library refuses
 raises ``PrismError``.
+
+A call's checks and its descriptor depend on its arguments' shapes, strides, types and devices alone; they are
+made once a signature and kept (``_plans``), so that a repeated call costs little more than its launch.
 """
 from __future__ import annotations
 
-import contextlib
-import functools
+import ctypes
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -33,9 +35,52 @@ _PAIRS = {"interleaved": 0, "half": 1}
 
 
 # ------------------------------------------------------------------ shared checks
+_plans = {}             # signature -> the checked call: descriptor, output shapes
+_MAX_PLANS = 2048
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _keep(key, plan):
+    if len(_plans) >= _MAX_PLANS:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+class _Plan:
+    """A checked call.  ``copy``: an argument's layout is not one that the library walks, so the arguments are laid
+    out anew and the call is made with those."""
+    __slots__ = ("desc", "addr", "index", "copy", "ws_bytes", "a", "b", "c")
+
+    def __init__(self, desc, dev, copy=False):
+        self.desc, self.addr, self.index, self.copy = desc, ctypes.addressof(desc), dev.index, copy
+        self.ws_bytes = 0
+        self.a = self.b = self.c = None
+
+
+def _current(index):
+    return torch._C._cuda_getDevice() == index
+
+
+def _stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _check(name, code):
+    if code:
+        raise _abi.PrismError(name, code)
 
 
 def _same_device(dev, *tensors):
@@ -45,51 +90,67 @@ def _same_device(dev, *tensors):
             raise ValueError(f"tensors on {dev} and {t.device}")
 
 
-def _on(dev):
-    """The device as the current one, where it is another."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _rows(t, C, what):
-    """t as rows of C contiguous channels, copied only where it cannot be viewed so."""
-    if t.dim() == 0 or t.shape[-1] != C:
-        raise ValueError(f"{what} must be [..., {C}], not {tuple(t.shape)}")
-    if t.dim() != 2:
-        t = t.reshape(-1, C) if t.numel() or C == 0 else t.new_empty(_count(t), C)
-    if (C > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < C):
-        t = t.contiguous()
-    return t
-
-
-def _count(t):
+def _count(shape):
     n = 1
-    for s in t.shape[:-1]:
+    for s in shape[:-1]:
         n *= s
     return n
 
 
-def _ld(t):
-    """Row stride for the library (0: dense rows)."""
-    return t.stride(0) if t is not None and t.shape[0] > 1 else 0
+def _row_stride(t):
+    """Elements between rows of C contiguous channels, 0 for dense ones or one row; None where t is not laid out so."""
+    shape, stride = t.shape, t.stride()
+    C = shape[-1]
+    dims = [(n, s) for n, s in zip(shape[:-1], stride[:-1]) if n != 1]
+    if any(n == 0 for n, _ in dims):
+        return 0
+    if C > 1 and stride[-1] != 1:
+        return None
+    for (_, s), (n, inner) in zip(dims, dims[1:]):
+        if s != n * inner:
+            return None
+    if not dims:
+        return 0
+    return dims[-1][1] if dims[-1][1] >= C else None
+
+
+def _like(t, dtype):
+    """A dense tensor of t's shape."""
+    if t.dtype == dtype and t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(*t.shape, dtype=dtype, device=t.device)
+
+
+def _dense(t):
+    """t where its rows lie evenly, else a copy."""
+    return t if t is None or _row_stride(t) is not None else t.contiguous()
 
 
 def _bytes(t):
     """First and last address of a tensor's elements."""
     a = t.data_ptr()
+    if t.is_contiguous():
+        return a, a + t.numel() * t.element_size()
     return a, a + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
 def _apart(a, b):
-    """Whether two tensors of rows share no element: other memory, or other columns of the same rows."""
+    """Whether two tensors share no element: other memory, or other columns of the same rows."""
     if a is None or b is None or not a.numel() or not b.numel():
         return True
     (a0, a1), (b0, b1) = _bytes(a), _bytes(b)
     if a1 <= b0 or b1 <= a0:
         return True
-    step = a.stride(0) * a.element_size()
-    if a.dim() < 2 or step != b.stride(0) * b.element_size() or step <= 0:
+    if a.dim() < 2 or a.dim() != b.dim():
         return False
-    (_, ae), (_, be) = _bytes(a[0]), _bytes(b[0])
+    # the dimensions that hold more than a row, from the outermost on, have to run alike
+    while a.dim() > 1 and (a.dim() > 2 and a.stride(0) == a.shape[1] * a.stride(1)
+                           and b.stride(0) == b.shape[1] * b.stride(1)):
+        a, b = a.flatten(0, 1), b.flatten(0, 1)
+    step = a.stride(0) * a.element_size()
+    if step != b.stride(0) * b.element_size() or step <= 0:
+        return False
+    (a0, ae), (b0, be) = _bytes(a[0]), _bytes(b[0])
     off = (b0 - a0) % step
     return ae - a0 <= off and off + be - b0 <= step
 
@@ -100,12 +161,19 @@ def _itself(a, b):
 
 def _check_out(out, what, allowed, *others):
     """An output may be the tensor ``allowed`` itself, and has to be apart from all others."""
+    o0, o1 = _bytes(out)
+    near = False
+    for t in (allowed, *others):
+        if t is not None:
+            t0, t1 = _bytes(t)
+            near = near or (t0 < o1 and o0 < t1)
+    if not near:
+        return
+    if allowed is not None and not _apart(out, allowed):
+        _need(_itself(out, allowed), f"{what} overlaps an input without being it")
     for t in others:
-        if t is not None and not _apart(out, t) and not (t is allowed or (allowed is not None and _itself(t, allowed))
-                                                         and _itself(out, t)):
-            raise ValueError(f"{what} overlaps another argument")
-    if allowed is not None and not _apart(out, allowed) and not _itself(out, allowed):
-        raise ValueError(f"{what} overlaps an input without being it")
+        _need(_apart(out, t) or (allowed is not None and _itself(out, allowed) and _itself(t, allowed)),
+              f"{what} overlaps another argument")
 
 
 def _refuse_capture(name, instead):
@@ -118,44 +186,53 @@ def _wants_graph(*tensors):
 
 
 # ------------------------------------------------------------------ block norms
-@functools.lru_cache(maxsize=256)
-def _norm_desc(*fields):
-    d = _abi.BlockNormT(*fields)
-    return d, _abi.block_norm_ws_bytes(d)
-
-
 def _vector(v, shape, what):
     if v is None:
-        return None
-    if v.dtype != torch.float32:
-        raise ValueError(f"{what} must be float32, not {v.dtype}")
-    if tuple(v.shape) != shape:
-        raise ValueError(f"{what} must be {shape}, not {tuple(v.shape)}")
-    if len(shape) == 1:
-        return v.contiguous()
-    return v if (shape[1] == 1 or v.stride(1) == 1) and (shape[0] < 2 or v.stride(0) >= shape[1]) else v.contiguous()
+        return
+    _need(v.dtype == torch.float32, f"{what} must be float32, not {v.dtype}")
+    _need(tuple(v.shape) == shape, f"{what} must be {shape}, not {tuple(v.shape)}")
 
 
-def _norm_setup(x, h, gate, post_weight, weight, bias, scale, shift, norm, post_norm, rows_per_group, branch):
+def _norm_plan(key, x, h, gate, post_weight, weight, bias, scale, shift, norm, post_norm, eps, res_scale, rows_per_group,
+               branch, rows):
+    """The call's plan; ``rows``: its other tensors like x, as (field of the descriptor, name, tensor, type)."""
     _need(norm in _NORMS, f"norm is 'layer', 'rms' or None, not {norm!r}")
     _need(post_norm in _NORMS, f"post_norm is 'layer', 'rms' or None, not {post_norm!r}")
     _need(x.dim() >= 1 and x.shape[-1] >= 1, f"x must be [..., C], not {tuple(x.shape)}")
     _need(x.dtype in _DT and branch in _DT, f"float32 or bfloat16, not {x.dtype} and {branch}")
-    C = x.shape[-1]
-    _same_device(x.device, h, gate, post_weight, weight, bias, scale, shift)
+    C, R, dev = x.shape[-1], _count(x.shape), x.device
+    _same_device(dev, h, gate, post_weight, weight, bias, scale, shift, *(t for _, _, t, _ in rows))
     if h is not None:
         _need(h.shape == x.shape, f"h must have x's shape {tuple(x.shape)}, not {tuple(h.shape)}")
         _need(h.dtype == branch, f"h is {h.dtype} and the next branch {branch}")
-    R = _count(x)
+    for _, what, t, dt in rows:
+        _need(t is None or (t.shape == x.shape and t.dtype == dt),
+              f"{what} must be {dt} of shape {tuple(x.shape)}")
     rpg = rows_per_group
     if rpg is None:
         rpg = x.shape[-2] if x.dim() > 2 else R
     _need(rpg >= 1 or R == 0, "rows_per_group must be at least 1")
     rpg = max(1, int(rpg))
     G = -(-R // rpg)
-    return (C, R, rpg, _vector(gate, (G, C), "gate"), _vector(post_weight, (C,), "post_weight"),
-            _vector(weight, (C,), "weight"), _vector(bias, (C,), "bias"), _vector(scale, (G, C), "scale"),
-            _vector(shift, (G, C), "shift"))
+    for v, shape, what in ((gate, (G, C), "gate"), (scale, (G, C), "scale"), (shift, (G, C), "shift"),
+                           (post_weight, (C,), "post_weight"), (weight, (C,), "weight"), (bias, (C,), "bias")):
+        _vector(v, shape, what)
+    lds = dict.fromkeys(("x", "h", "z", "y", "dx", "dh", "dz", "dy", "gate", "scale", "shift"), 0)
+    copy = any(v is not None and v.stride(0) != 1 and C > 1 for v in (post_weight, weight, bias))
+    for field, t in ([("x", x), ("h", h), ("gate", gate), ("scale", scale), ("shift", shift)]
+                     + [(f, t) for f, _, t, _ in rows]):
+        if t is not None:
+            ld = _row_stride(t)
+            copy = copy or ld is None
+            lds[field] = ld or 0
+    if rows and rows[0][0] == "dz":                # the backward reads the stream as z
+        lds["z"], lds["x"] = lds["x"], 0
+    desc = _abi.BlockNormT(R, rpg, C, _DT[x.dtype], _DT[branch], _NORMS[norm], _NORMS[post_norm], eps, res_scale,
+                           *lds.values())
+    p = _Plan(desc, dev, copy)
+    p.ws_bytes = _abi.block_norm_ws_bytes(desc)
+    p.a, p.b = _NORMS[norm] != 0, (G, C)
+    return _keep(key, p)
 
 
 def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=None, scale=None, shift=None,
@@ -169,37 +246,46 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
     three or more, else all rows); weight, bias and post_weight float32 [C].  ``norm=None`` gives no y.  y has
     ``out_dtype`` (default: h's type, else x's).  ``z`` and ``y`` may be given as outputs; z may be x itself.
     """
-    branch = out_dtype or (h if h is not None else x).dtype
-    C, R, rpg, gate, post_weight, weight, bias, scale, shift = _norm_setup(
-        x, h, gate, post_weight, weight, bias, scale, shift, norm, post_norm, rows_per_group, branch)
-    dev = x.device
-    given = []
-    for t, dt, what in ((z, x.dtype, "z"), (y, branch, "y")):
-        if t is not None:
-            _need(t.shape == x.shape and t.dtype == dt and t.device == dev,
-                  f"{what} must be {dt} of shape {tuple(x.shape)} on {dev}")
-            v = t.flatten(0, -2) if t.dim() > 1 else t.view(1, C)
-            _need(not t.numel() or (v.data_ptr() == t.data_ptr() and (C == 1 or v.stride(1) == 1)
-                                    and (v.shape[0] < 2 or v.stride(0) >= C)), f"{what}'s rows must lie evenly")
-            given.append((v, what))
-    _need(z is None or h is not None, "without h there is no z to write")
-    _need(y is None or norm not in (None, "none"), "without a norm there is no y to write")
-    xr, hr = _rows(x, C, "x"), None if h is None else _rows(h, C, "h")
-    for i, (v, what) in enumerate(given):
-        _check_out(v, what, xr if what == "z" else None, xr, hr, gate, post_weight, weight, bias, scale, shift,
-                   *(o for o, _ in given[:i]))
-    with _on(dev):
-        has_y = norm not in (None, "none")
-        if z is None and h is not None:
-            z = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        if y is None and has_y:
-            y = torch.empty(x.shape, dtype=branch, device=dev)
-        zr, yr = (None if t is None else t.view(-1, C) if t.is_contiguous() and t.numel() else t.flatten(0, -2)
-                  if t.dim() > 1 else t.view(1, C) for t in (z, y))
-        d, _ = _norm_desc(R, rpg, C, _DT[x.dtype], _DT[branch], _NORMS[norm], _NORMS[post_norm], eps, res_scale,
-                          _ld(xr), _ld(hr), _ld(zr), _ld(yr), 0, 0, 0, 0, _ld(gate), _ld(scale), _ld(shift))
-        _abi.prism_block_norm_fwd(d, xr, hr, gate, post_weight, weight, bias, scale, shift, zr, yr)
+    key = ("norm", x.shape, x.stride(), x.dtype, x.device, _sig(h), _sig(gate), _sig(post_weight), _sig(weight), _sig(bias),
+           _sig(scale), _sig(shift), norm, post_norm, eps, res_scale, rows_per_group, out_dtype, _sig(z), _sig(y))
+    p = _plans.get(key)
+    if p is None:
+        branch = out_dtype or (h if h is not None else x).dtype
+        _need(z is None or h is not None, "without h there is no z to write")
+        _need(y is None or norm not in (None, "none"), "without a norm there is no y to write")
+        for t, what in ((z, "z"), (y, "y")):
+            _need(t is None or t.dim() < 1 or _row_stride(t) is not None, f"{what}'s rows must lie evenly")
+        p = _norm_plan(key, x, h, gate, post_weight, weight, bias, scale, shift, norm, post_norm, eps, res_scale,
+                       rows_per_group, branch, (("z", "z", z, x.dtype), ("y", "y", y, branch)))
+        p.c = branch
+    if p.copy:
+        x0 = x
+        vecs = [None if v is None else v.contiguous() for v in (post_weight, weight, bias)]
+        x, h, gate, scale, shift = (_dense(t) for t in (x, h, gate, scale, shift))
+        zo, yo = norm_forward(x, h, gate=gate, post_weight=vecs[0], weight=vecs[1], bias=vecs[2], scale=scale,
+                              shift=shift, norm=norm, post_norm=post_norm, eps=eps, res_scale=res_scale,
+                              rows_per_group=rows_per_group, out_dtype=out_dtype, z=z, y=y)
+        return (x0 if h is None else zo), yo
+    if not _current(p.index):
+        with torch.cuda.device(p.index):
+            return norm_forward(x, h, gate=gate, post_weight=post_weight, weight=weight, bias=bias, scale=scale,
+                                shift=shift, norm=norm, post_norm=post_norm, eps=eps, res_scale=res_scale,
+                                rows_per_group=rows_per_group, out_dtype=out_dtype, z=z, y=y)
+    if z is not None:
+        _check_out(z, "z", x, h, gate, post_weight, weight, bias, scale, shift)
+    elif h is not None:
+        z = _like(x, x.dtype)
+    if y is not None:
+        _check_out(y, "y", None, x, h, gate, post_weight, weight, bias, scale, shift, z)
+    elif p.a:
+        y = _like(x, p.c)
+    _check("prism_block_norm_fwd", _abi.lib().prism_block_norm_fwd(
+        p.addr, x.data_ptr(), _ptr(h), _ptr(gate), _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(scale),
+        _ptr(shift), _ptr(z), _ptr(y), _stream(p.index)))
     return (x if h is None else z), y
+
+
+_NORM_GRADS = ("dgate", "dscale", "dshift", "dpost_weight", "dweight", "dbias")      # [groups, C], then [C]
 
 
 def norm_backward(z, h, dz, dy, *, gate=None, post_weight=None, weight=None, bias=None, scale=None, norm="layer",
@@ -211,36 +297,50 @@ def norm_backward(z, h, dz, dy, *, gate=None, post_weight=None, weight=None, bia
     scale, ``dshift``; the others are None.  ``wants``: names of the vectors' gradients to take instead
     (``dshift`` needs no vector).
     """
-    branch = (dy if dy is not None else h if h is not None else z).dtype
-    C, R, rpg, gate, post_weight, weight, bias, scale, _ = _norm_setup(
-        z, h, gate, post_weight, weight, bias, scale, None, norm, post_norm, rows_per_group, branch)
-    dev, G = z.device, -(-R // rpg)
-    _same_device(dev, dz, dy)
-    has_y = norm not in (None, "none")
-    _need(not has_y or dy is not None, "a norm's backward needs dy")
-    _need(has_y or dz is not None, "without a norm the backward needs dz")
-    for t, dt, what in ((dz, z.dtype, "dz"), (dy, branch, "dy")):
-        _need(t is None or (t.shape == z.shape and t.dtype == dt), f"{what} must be {dt} of shape {tuple(z.shape)}")
-    if wants is None:
-        wants = [n for n, v in (("dgate", gate), ("dpost_weight", post_weight), ("dweight", weight), ("dbias", bias),
-                                ("dscale", scale), ("dshift", scale)) if v is not None]
-    else:
-        for n in wants:
-            _need(n in ("dgate", "dpost_weight", "dweight", "dbias", "dscale", "dshift"), f"no gradient {n!r}")
-    zr, hr, dzr, dyr = (None if t is None else _rows(t, C, n) for t, n in ((z, "z"), (h, "h"), (dz, "dz"), (dy, "dy")))
-    with _on(dev):
-        g = dict.fromkeys(("dx", "dh", "dgate", "dpost_weight", "dweight", "dbias", "dscale", "dshift"))
-        g["dx"] = torch.empty(z.shape, dtype=z.dtype, device=dev)
-        if h is not None:
-            g["dh"] = torch.empty(z.shape, dtype=branch, device=dev)
-        for n in wants:
-            g[n] = torch.empty((G, C) if n in ("dgate", "dscale", "dshift") else (C,), dtype=torch.float32, device=dev)
-        d, ws_bytes = _norm_desc(R, rpg, C, _DT[z.dtype], _DT[branch], _NORMS[norm], _NORMS[post_norm], eps,
-                                 res_scale, 0, _ld(hr), _ld(zr), 0, 0, 0, _ld(dzr), _ld(dyr), _ld(gate), _ld(scale), 0)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if wants else None
-        _abi.prism_block_norm_bwd(d, zr, hr, gate, post_weight, weight, bias, scale, dzr, dyr, g["dx"], g["dh"],
-                                  g["dgate"], g["dpost_weight"], g["dweight"], g["dbias"], g["dscale"], g["dshift"],
-                                  ws, ws_bytes if wants else 0)
+    if wants is not None:
+        wants = tuple(wants)
+    key = ("dnorm", z.shape, z.stride(), z.dtype, z.device, _sig(h), _sig(dz), _sig(dy), _sig(gate), _sig(post_weight),
+           _sig(weight), _sig(bias), _sig(scale), norm, post_norm, eps, res_scale, rows_per_group, wants)
+    p = _plans.get(key)
+    if p is None:
+        branch = (dy if dy is not None else h if h is not None else z).dtype
+        has_y = norm not in (None, "none")
+        _need(not has_y or dy is not None, "a norm's backward needs dy")
+        _need(has_y or dz is not None, "without a norm the backward needs dz")
+        have = dict(dgate=gate, dscale=scale, dshift=scale, dpost_weight=post_weight, dweight=weight, dbias=bias)
+        names = [n for n in _NORM_GRADS if have[n] is not None] if wants is None else wants
+        for n in names:
+            _need(n in _NORM_GRADS, f"no gradient {n!r}")
+        p = _norm_plan(key, z, h, gate, post_weight, weight, bias, scale, None, norm, post_norm, eps, res_scale,
+                       rows_per_group, branch, (("dz", "dz", dz, z.dtype), ("dy", "dy", dy, branch)))
+        p.a, p.c = branch, ([n for n in _NORM_GRADS[:3] if n in names], [n for n in _NORM_GRADS[3:] if n in names])
+    if p.copy:
+        vecs = [None if v is None else v.contiguous() for v in (post_weight, weight, bias)]
+        z, h, dz, dy, gate, scale = (_dense(t) for t in (z, h, dz, dy, gate, scale))
+        return norm_backward(z, h, dz, dy, gate=gate, post_weight=vecs[0], weight=vecs[1], bias=vecs[2], scale=scale,
+                             norm=norm, post_norm=post_norm, eps=eps, res_scale=res_scale,
+                             rows_per_group=rows_per_group, wants=wants)
+    if not _current(p.index):
+        with torch.cuda.device(p.index):
+            return norm_backward(z, h, dz, dy, gate=gate, post_weight=post_weight, weight=weight, bias=bias, scale=scale,
+                                 norm=norm, post_norm=post_norm, eps=eps, res_scale=res_scale,
+                                 rows_per_group=rows_per_group, wants=wants)
+    dev = z.device
+    g = dict.fromkeys(("dx", "dh", "dgate", "dpost_weight", "dweight", "dbias", "dscale", "dshift"))
+    g["dx"] = _like(z, z.dtype)
+    if h is not None:
+        g["dh"] = _like(z, p.a)
+    groups, vectors = p.c
+    G, C = p.b
+    for n in groups:
+        g[n] = torch.empty(G, C, dtype=torch.float32, device=dev)
+    for n in vectors:
+        g[n] = torch.empty(C, dtype=torch.float32, device=dev)
+    ws = torch.empty(p.ws_bytes, dtype=torch.uint8, device=dev) if groups or vectors else None
+    _check("prism_block_norm_bwd", _abi.lib().prism_block_norm_bwd(
+        p.addr, z.data_ptr(), _ptr(h), _ptr(gate), _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(scale), _ptr(dz),
+        _ptr(dy), _ptr(g["dx"]), _ptr(g["dh"]), _ptr(g["dgate"]), _ptr(g["dpost_weight"]), _ptr(g["dweight"]),
+        _ptr(g["dbias"]), _ptr(g["dscale"]), _ptr(g["dshift"]), _ptr(ws), p.ws_bytes, _stream(p.index)))
     return g
 
 
@@ -289,12 +389,6 @@ def norm(x, h=None, *, gate=None, post_weight=None, weight=None, bias=None, scal
 
 
 # ------------------------------------------------------------------ head norm and rotation
-@functools.lru_cache(maxsize=256)
-def _rotate_desc(*fields):
-    d = _abi.RotateT(*fields)
-    return d, _abi.head_rotate_ws_bytes(d)
-
-
 def rotation_table(grid, axes, base=10000.0, device="cuda", positions=None):
     """The (cos, sin) rows that ``rotate`` reads: for each axis of ``grid`` = (T, H, W) a row for each place with
     ``axes`` = (pairs_t, pairs_h, pairs_w) pairs, pair i of n at place p turned by p base^(-i/n).  ``positions``:
@@ -309,44 +403,69 @@ def rotation_table(grid, axes, base=10000.0, device="cuda", positions=None):
     return torch.cat(parts).float().to(device)
 
 
-def _heads(t, what):
-    """t as [tokens, heads, d] rows that the library can walk, copied where it cannot be viewed so."""
-    _need(t.dim() == 3, f"{what} must be [tokens, heads, head_dim], not {tuple(t.shape)}")
+def _head_stride(t):
+    """Elements between tokens of t [tokens, heads, d], 0 for dense ones; None where the library cannot walk it."""
     n, h, d = t.shape
-    step = 16 // t.element_size()
-    if ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)
-            or (n > 1 and (t.stride(0) < h * d or t.stride(0) % step)) or t.data_ptr() % 16):
-        t = t.contiguous()
-        if t.data_ptr() % 16:
-            t = t.clone()
-    return t
+    s = t.stride()
+    if t.numel() == 0:
+        return 0
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        return None
+    if n == 1:
+        return 0
+    return s[0] if s[0] >= h * d and s[0] * t.element_size() % 16 == 0 else None
 
 
-def _rotate_setup(sides, table, grid, axes, weights, norm, pairs):
+def _aligned(t):
+    """A dense copy of t, on 16 bytes (heads laid out otherwise, or starting elsewhere)."""
+    if t is None or (_head_stride(t) is not None and t.data_ptr() % 16 == 0):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _on16(*tensors):
+    m = 0
+    for t in tensors:
+        if t is not None:
+            m |= t.data_ptr()
+    return m % 16 == 0
+
+
+def _rotate_plan(key, ins, outs, table, grid, axes, weights, norm, eps, pairs):
+    """ins, outs: pairs of tensors (Q's, K's) by descriptor fields, the first of ins deciding the shapes."""
     _need(pairs in _PAIRS, f"pairs is 'interleaved' or 'half', not {pairs!r}")
     _need(len(grid) == 3 and len(axes) == 3, "grid and axes have three entries: (T, H, W)")
-    first = next((t for t in sides if t is not None), None)
-    _need(first is not None, "neither Q nor K")
-    _same_device(first.device, table, *sides, *weights)
-    for t in sides:
-        _need(t is None or t.dim() == 3, "Q and K must be [tokens, heads, head_dim]")
-        _need(t is None or (t.shape[0] == first.shape[0] and t.shape[2] == first.shape[2] and t.dtype == first.dtype),
+    tensors = [t for f, pair in (*ins, *outs) for t in pair if t is not None]
+    _need(tensors, "neither Q nor K")
+    first = tensors[0]
+    _same_device(first.device, table, *tensors, *weights)
+    for t in tensors:
+        _need(t.dim() == 3, "Q and K must be [tokens, heads, head_dim]")
+        _need(t.shape[0] == first.shape[0] and t.shape[2] == first.shape[2] and t.dtype == first.dtype,
               "Q and K must agree in tokens, head_dim and type")
     _need(first.dtype in _DT, f"float32 or bfloat16, not {first.dtype}")
     rows = sum(n * p for n, p in zip(grid, axes))
     _need(table.dtype == torch.float32 and tuple(table.shape) == (rows, 2),
           f"table must be float32 [{rows}, 2], not {table.dtype} {tuple(table.shape)}")
-    ws = [_vector(w, (first.shape[2],), "a head's weight") for w in weights]
-    _need(norm or (ws[0] is None and ws[1] is None), "weights without a norm")
-    ws = [w if w is None or w.data_ptr() % 16 == 0 else w.clone() for w in ws]
-    table = table.contiguous()
-    return first, table if table.data_ptr() % 16 == 0 else table.clone(), ws
-
-
-def _rotate_fields(first, sides, grid, axes, norm, eps, pairs, lds):
-    hq, hk = (0 if t is None else t.shape[1] for t in sides)
-    return (first.shape[0], *grid, hq, hk, first.shape[2], *axes, _PAIRS[pairs], _DT[first.dtype], int(bool(norm)), eps,
-            *lds)
+    for w in weights:
+        _vector(w, (first.shape[2],), "a head's weight")
+        _need(norm or w is None, "weights without a norm")
+    copy = not table.is_contiguous() or any(w is not None and w.stride(0) != 1 for w in weights)
+    lds = {}
+    for fields, pair in (*ins, *outs):
+        for f, t in zip(fields, pair):
+            ld = 0 if t is None else _head_stride(t)
+            copy = copy or ld is None
+            lds[f] = ld or 0
+    heads = [0 if t is None else t.shape[1] for t in ins[0][1]]
+    for _, pair in (*ins[1:], *outs):
+        for t, n in zip(pair, heads):
+            _need(t is None or t.shape[1] == n, "Q and K must be like their gradients and results")
+    desc = _abi.RotateT(first.shape[0], *grid, *heads, first.shape[2], *axes, _PAIRS[pairs], _DT[first.dtype],
+                        int(bool(norm)), eps, *(lds.get(f, 0) for f in ("q", "k", "qo", "ko", "dq", "dk")))
+    p = _Plan(desc, first.device, copy)
+    p.ws_bytes = _abi.head_rotate_ws_bytes(desc)
+    return _keep(key, p)
 
 
 def rotate_forward(Q, K, table, *, grid, axes, q_weight=None, k_weight=None, norm=True, eps=1e-6, pairs="interleaved",
@@ -358,27 +477,41 @@ def rotate_forward(Q, K, table, *, grid, axes, q_weight=None, k_weight=None, nor
     'interleaved' (channels 2i, 2i + 1) or 'half' (i, i + d/2).  Q or K may be None, and have different numbers of
     heads.  ``out`` = (Qr, Kr) takes the results, and may be (Q, K) themselves.
     """
-    first, table, ws = _rotate_setup((Q, K), table, grid, axes, (q_weight, k_weight), norm, pairs)
-    dev = first.device
-    src = [None if t is None else _heads(t, "Q or K") for t in (Q, K)]
-    if out is not None:
-        _need(len(out) == 2, "out is (Qr, Kr)")
-        for i, (o, t, s) in enumerate(zip(out, (Q, K), src)):
-            _need((o is None) == (t is None), "out must have a tensor for each of Q and K")
-            if o is None:
-                continue
-            _need(o.shape == t.shape and o.dtype == t.dtype and o.device == dev, "out must be like Q and K")
-            _need(not o.numel() or _heads(o, "out") is o, "out's heads must lie densely on 16-byte boundaries")
-            _check_out(o, "out", s, table, *ws, *(out[:i]))
-            # one tensor as Q and K would be read by one side while the other writes it
-            _need(_apart(o, src[1 - i]), "out overlaps the other of Q and K")
-    with _on(dev):
-        if out is None:
-            out = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (Q, K)]
-        d, _ = _rotate_desc(*_rotate_fields(first, (Q, K), grid, axes, norm, eps, pairs,
-                                            (_ld(src[0]), _ld(src[1]), _ld(out[0]), _ld(out[1]), 0, 0)))
-        _abi.prism_head_rotate_fwd(d, src[0], src[1], ws[0], ws[1], table, out[0], out[1])
-    return tuple(out)
+    oq, ok = (None, None) if out is None else out
+    key = ("rotate", _sig(Q), _sig(K), _sig(table), tuple(grid), tuple(axes), _sig(q_weight), _sig(k_weight), norm, eps,
+           pairs, _sig(oq), _sig(ok))
+    p = _plans.get(key)
+    if p is None:
+        _need(out is None or ((oq is None) == (Q is None) and (ok is None) == (K is None)),
+              "out must have a tensor for each of Q and K")
+        for o in (oq, ok):
+            _need(o is None or (o.dim() == 3 and _head_stride(o) is not None),
+                  "out's heads must lie densely on 16-byte boundaries")
+        p = _rotate_plan(key, ((("q", "k"), (Q, K)),), ((("qo", "ko"), (oq, ok)),), table, grid, axes,
+                         (q_weight, k_weight), norm, eps, pairs)
+    if p.copy or not _on16(Q, K, table, q_weight, k_weight):
+        vecs = [None if v is None else v.clone(memory_format=torch.contiguous_format) for v in (q_weight, k_weight)]
+        _need(_on16(oq, ok), "out must lie on 16-byte boundaries")
+        return rotate_forward(_aligned(Q), _aligned(K), table.clone(memory_format=torch.contiguous_format), grid=grid,
+                              axes=axes, q_weight=vecs[0], k_weight=vecs[1], norm=norm, eps=eps, pairs=pairs, out=out)
+    if not _current(p.index):
+        with torch.cuda.device(p.index):
+            return rotate_forward(Q, K, table, grid=grid, axes=axes, q_weight=q_weight, k_weight=k_weight, norm=norm,
+                                  eps=eps, pairs=pairs, out=out)
+    if out is None:
+        oq = None if Q is None else _like(Q, Q.dtype)
+        ok = None if K is None else _like(K, K.dtype)
+    else:
+        # one tensor as Q and K would be read by one side while the other writes it
+        for o, own, other in ((oq, Q, K), (ok, K, Q)):
+            if o is not None:
+                _check_out(o, "out", own, table, q_weight, k_weight)
+                _need(_apart(o, other), "out overlaps the other of Q and K")
+        _need(_apart(oq, ok), "the outputs overlap")
+    _check("prism_head_rotate_fwd", _abi.lib().prism_head_rotate_fwd(
+        p.addr, _ptr(Q), _ptr(K), _ptr(q_weight), _ptr(k_weight), table.data_ptr(), _ptr(oq), _ptr(ok),
+        _stream(p.index)))
+    return oq, ok
 
 
 def rotate_backward(Q, K, dQr, dKr, table, *, grid, axes, q_weight=None, k_weight=None, norm=True, eps=1e-6,
@@ -386,33 +519,49 @@ def rotate_backward(Q, K, dQr, dKr, table, *, grid, axes, q_weight=None, k_weigh
     """Gradients of ``rotate_forward`` from its inputs Q, K and its outputs' gradients: a dict of ``dQ``, ``dK`` and,
     for the weights that are given, ``dq_weight``, ``dk_weight`` (``wants``: names of these to take instead); the
     others are None.  Without a norm Q and K are not read and may be None."""
-    first, table, ws = _rotate_setup((dQr, dKr), table, grid, axes, (q_weight, k_weight), norm, pairs)
-    dev = first.device
-    _same_device(dev, Q, K)
-    xs, drs = [], []
-    for x, dr in ((Q, dQr), (K, dKr)):
-        _need(x is None or (dr is not None and x.shape == dr.shape and x.dtype == dr.dtype),
-              "Q and K must be like their gradients")
-        _need(dr is None or x is not None or not norm, "the norm's backward needs Q and K")
-        xs.append(None if x is None or not norm else _heads(x, "Q or K"))
-        drs.append(None if dr is None else _heads(dr, "dQr or dKr"))
-    if wants is None:
-        wants = [n for n, w in (("dq_weight", ws[0]), ("dk_weight", ws[1])) if w is not None]
-    for n in wants:
-        _need(n in ("dq_weight", "dk_weight") and norm, f"no gradient {n!r} here")
-        _need((dQr if n == "dq_weight" else dKr) is not None, f"no gradient {n!r} here")
+    if wants is not None:
+        wants = tuple(wants)
+    if not norm:
+        Q = K = None
+    key = ("drotate", _sig(Q), _sig(K), _sig(dQr), _sig(dKr), _sig(table), tuple(grid), tuple(axes), _sig(q_weight),
+           _sig(k_weight), norm, eps, pairs, wants)
+    p = _plans.get(key)
+    if p is None:
+        for x, dr in ((Q, dQr), (K, dKr)):
+            _need(x is None or dr is not None, "Q and K must be like their gradients")
+            _need(dr is None or x is not None or not norm, "the norm's backward needs Q and K")
+        names = wants if wants is not None else [n for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight))
+                                                 if w is not None]
+        for n in names:
+            _need(n in ("dq_weight", "dk_weight") and norm and (dQr if n == "dq_weight" else dKr) is not None,
+                  f"no gradient {n!r} here")
+        p = _rotate_plan(key, ((("dq", "dk"), (dQr, dKr)), (("q", "k"), (Q, K))), (), table, grid, axes,
+                         (q_weight, k_weight), norm, eps, pairs)
+        p.a = names
+    if p.copy or not _on16(Q, K, dQr, dKr, table, q_weight, k_weight):
+        vecs = [None if v is None else v.clone(memory_format=torch.contiguous_format) for v in (q_weight, k_weight)]
+        return rotate_backward(_aligned(Q), _aligned(K), _aligned(dQr), _aligned(dKr),
+                               table.clone(memory_format=torch.contiguous_format), grid=grid, axes=axes,
+                               q_weight=vecs[0], k_weight=vecs[1], norm=norm, eps=eps, pairs=pairs, wants=wants)
+    if not _current(p.index):
+        with torch.cuda.device(p.index):
+            return rotate_backward(Q, K, dQr, dKr, table, grid=grid, axes=axes, q_weight=q_weight, k_weight=k_weight,
+                                   norm=norm, eps=eps, pairs=pairs, wants=wants)
+    dev = table.device
     g = dict.fromkeys(("dQ", "dK", "dq_weight", "dk_weight"))
-    with _on(dev):
-        for n, dr in (("dQ", dQr), ("dK", dKr)):
-            if dr is not None:
-                g[n] = torch.empty(dr.shape, dtype=dr.dtype, device=dev)
-        for n in wants:
-            g[n] = torch.empty(first.shape[2], dtype=torch.float32, device=dev)
-        d, ws_bytes = _rotate_desc(*_rotate_fields(first, (dQr, dKr), grid, axes, norm, eps, pairs,
-                                                   (_ld(xs[0]), _ld(xs[1]), 0, 0, _ld(drs[0]), _ld(drs[1]))))
-        buf = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if wants else None
-        _abi.prism_head_rotate_bwd(d, xs[0], xs[1], ws[0], ws[1], table, drs[0], drs[1], g["dQ"], g["dK"],
-                                   g["dq_weight"], g["dk_weight"], buf, ws_bytes if wants else 0)
+    if dQr is not None:
+        g["dQ"] = _like(dQr, dQr.dtype)
+    if dKr is not None:
+        g["dK"] = _like(dKr, dKr.dtype)
+    ws = None
+    if p.a:
+        d = p.desc.head_dim
+        for n in p.a:
+            g[n] = torch.empty(d, dtype=torch.float32, device=dev)
+        ws = torch.empty(p.ws_bytes, dtype=torch.uint8, device=dev)
+    _check("prism_head_rotate_bwd", _abi.lib().prism_head_rotate_bwd(
+        p.addr, _ptr(Q), _ptr(K), _ptr(q_weight), _ptr(k_weight), table.data_ptr(), _ptr(dQr), _ptr(dKr), _ptr(g["dQ"]),
+        _ptr(g["dK"]), _ptr(g["dq_weight"]), _ptr(g["dk_weight"]), _ptr(ws), p.ws_bytes, _stream(p.index)))
     return g
 
 
@@ -457,25 +606,23 @@ class ExpertPlan:
     where there is none.  All int32 on the device; ``rows_sorted`` is the host's bound on the sorted rows, of which
     offsets[experts] are in use.
     """
+    __slots__ = ("rows", "top_k", "experts", "align", "device", "rows_sorted", "counts", "offsets", "pos", "src",
+                 "_call", "_all", "_ws")
 
     def __init__(self, rows, top_k, experts, align, id_bytes, device):
-        self.desc, self.rows_sorted, self.ws_bytes = _expert_desc(rows, top_k, experts, align, id_bytes)
+        key = ("experts", rows, top_k, experts, align, id_bytes, device)
+        p = _plans.get(key)
+        if p is None:
+            p = _Plan(_abi.ExpertsT(rows, top_k, experts, align, id_bytes), device)
+            p.a, p.ws_bytes = _abi.expert_sizes(p.desc)
+            p.b = (experts, experts + 1, rows * top_k, p.a, p.ws_bytes // 4)
+            p.c = sum(p.b)
+            _keep(key, p)
+        self._call, self.rows_sorted = p, p.a
         self.rows, self.top_k, self.experts, self.align, self.device = rows, top_k, experts, align, device
-        # one allocation, its parts on 16-byte boundaries
-        sizes = (experts, experts + 1, rows * top_k, self.rows_sorted, self.ws_bytes // 4)
-        starts = [0]
-        for n in sizes:
-            starts.append(starts[-1] + (n + 3) // 4 * 4)
-        buf = torch.empty(starts[-1], dtype=torch.int32, device=device)
-        part = [buf[a:a + n] for a, n in zip(starts, sizes)]
-        self.counts, self.offsets, pos, self.src, self._ws = part
+        self._all = torch.empty(p.c, dtype=torch.int32, device=device)
+        self.counts, self.offsets, pos, self.src, self._ws = self._all.split_with_sizes(p.b)
         self.pos = pos.view(rows, top_k)
-
-
-@functools.lru_cache(maxsize=256)
-def _expert_desc(*fields):
-    d = _abi.ExpertsT(*fields)
-    return (d, *_abi.expert_sizes(d))
 
 
 def expert_plan(ids, experts, align=1) -> ExpertPlan:
@@ -483,55 +630,75 @@ def expert_plan(ids, experts, align=1) -> ExpertPlan:
     slot.  Each expert's rows start at a multiple of ``align``."""
     _need(ids.dim() == 2, f"ids must be [rows, top_k], not {tuple(ids.shape)}")
     _need(ids.dtype in (torch.int32, torch.int64), f"ids must be int32 or int64, not {ids.dtype}")
-    _same_device(ids.device)
-    ids = ids.contiguous()
-    with _on(ids.device):
-        p = ExpertPlan(ids.shape[0], ids.shape[1], int(experts), int(align), ids.element_size(), ids.device)
-        _abi.prism_expert_plan(p.desc, ids, p.counts, p.offsets, p.pos, p.src, p._ws if p.ws_bytes else None,
-                               p.ws_bytes)
+    dev = ids.device
+    _same_device(dev)
+    if not ids.is_contiguous():
+        ids = ids.contiguous()
+    if not _current(dev.index):
+        with torch.cuda.device(dev.index):
+            return expert_plan(ids, experts, align)
+    rows, top_k = ids.shape
+    p = ExpertPlan(rows, top_k, int(experts), int(align), ids.element_size(), dev)
+    c = p._call
+    _check("prism_expert_plan", _abi.lib().prism_expert_plan(
+        c.addr, ids.data_ptr(), p.counts.data_ptr(), p.offsets.data_ptr(), p.pos.data_ptr(), p.src.data_ptr(),
+        p._ws.data_ptr() if c.ws_bytes else None, c.ws_bytes, _stream(dev.index)))
     return p
 
 
-def _by_token(t, plan, C, what):
-    _need(t.dim() == 2 and t.shape[0] == plan.rows and (C is None or t.shape[1] == C),
+def _by_token(t, plan, C, dtype, what):
+    """Row stride of t [rows, C] (None: to be copied)."""
+    if t is None:
+        return 0
+    _need(t.dim() == 2 and t.shape[0] == plan.rows and t.shape[1] >= 1 and (C is None or t.shape[1] == C),
           f"{what} must be [{plan.rows}, channels], not {tuple(t.shape)}")
-    _need(t.dtype in _DT, f"float32 or bfloat16, not {t.dtype}")
+    _need(t.dtype in _DT and (dtype is None or t.dtype == dtype), f"{what} has type {t.dtype}")
     _same_device(plan.device, t)
-    return _rows(t, t.shape[1], what)
+    return _row_stride(t)
 
 
 def _sorted(t, plan, C, dtype, what):
-    _need(t.dim() == 2 and tuple(t.shape) == (plan.rows_sorted, C if C is not None else t.shape[1]),
-          f"{what} must be [{plan.rows_sorted}, channels], not {tuple(t.shape)}")
-    _need(t.dtype in _DT and (dtype is None or t.dtype == dtype), f"{what} has type {t.dtype}")
-    _same_device(plan.device, t)
-    return t
+    if t is not None:
+        _need(t.dim() == 2 and t.shape[0] == plan.rows_sorted and t.shape[1] >= 1 and (C is None or t.shape[1] == C),
+              f"{what} must be [{plan.rows_sorted}, channels], not {tuple(t.shape)}")
+        _need(t.dtype in _DT and (dtype is None or t.dtype == dtype), f"{what} has type {t.dtype}")
+        _same_device(plan.device, t)
 
 
 def _weights(w, plan):
-    if w is None:
-        return None
-    _need(w.dtype == torch.float32 and tuple(w.shape) == (plan.rows, plan.top_k),
-          f"weights must be float32 [{plan.rows}, {plan.top_k}]")
-    _same_device(plan.device, w)
-    return w.contiguous()
+    if w is not None:
+        _need(w.dtype == torch.float32 and tuple(w.shape) == (plan.rows, plan.top_k),
+              f"weights must be float32 [{plan.rows}, {plan.top_k}]")
+        _same_device(plan.device, w)
 
 
 def expert_dispatch(x, plan, *, out=None):
     """xs [rows_sorted, C]: x's rows [rows, C] copied to their slots' rows; the rows between an expert's last slot
     and the next multiple of ``align`` are 0, as are those behind the last expert.  A given ``out`` (dense, not
     overlapping x) keeps the rows behind the last expert as they are."""
-    xr = _by_token(x, plan, None, "x")
-    C = xr.shape[1]
-    with _on(plan.device):
-        clear = out is None
-        if clear:
-            out = torch.empty((plan.rows_sorted, C), dtype=x.dtype, device=plan.device)
-        else:
-            _need(_sorted(out, plan, C, x.dtype, "out").is_contiguous(), "out must be dense")
-            _check_out(out, "out", None, xr, plan.pos, plan.counts, plan.offsets)
-        _abi.prism_expert_dispatch(plan.desc, _DT[x.dtype], C, xr, _ld(xr), plan.pos, plan.counts, plan.offsets,
-                                   int(clear), out)
+    call = plan._call
+    key = ("dispatch", call, _sig(x), _sig(out))
+    p = _plans.get(key)
+    if p is None:
+        ld = _by_token(x, plan, None, None, "x")
+        _sorted(out, plan, x.shape[1], x.dtype, "out")
+        _need(out is None or out.is_contiguous(), "out must be dense")
+        p = _keep(key, _Plan(call.desc, plan.device, ld is None))
+        p.a = (_DT[x.dtype], x.shape[1], ld)
+    if p.copy:
+        return expert_dispatch(x.contiguous(), plan, out=out)
+    if not _current(p.index):
+        with torch.cuda.device(p.index):
+            return expert_dispatch(x, plan, out=out)
+    dt, C, ld = p.a
+    clear = out is None
+    if clear:
+        out = torch.empty(plan.rows_sorted, C, dtype=x.dtype, device=x.device)
+    else:
+        _check_out(out, "out", None, x, plan._all)
+    _check("prism_expert_dispatch", _abi.lib().prism_expert_dispatch(
+        p.addr, dt, C, x.data_ptr(), ld, plan.pos.data_ptr(), plan.counts.data_ptr(), plan.offsets.data_ptr(), clear,
+        out.data_ptr(), _stream(p.index)))
     return out
 
 
@@ -539,18 +706,32 @@ def expert_combine(ys, plan, weights=None, *, add=None, out=None):
     """out [rows, C]: add[t] + sum over t's choices j of weights[t, j] ys[pos[t, j]], without the dropped ones
     (weights float32 [rows, top_k], None: 1; add None: 0).  Summed in float32 in j's order, rounded once.  Without
     weights it is the gradient of ``expert_dispatch``.  ``out`` may be ``add`` itself."""
-    y = _sorted(ys, plan, None, None, "ys").contiguous()
-    C = y.shape[1]
-    w = _weights(weights, plan)
-    addr = None if add is None else _by_token(add, plan, C, "add")
-    _need(add is None or add.dtype == y.dtype, "add must have ys' type")
-    with _on(plan.device):
-        if out is None:
-            out = torch.empty((plan.rows, C), dtype=y.dtype, device=plan.device)
-        else:
-            _need(_by_token(out, plan, C, "out") is out and out.dtype == y.dtype, "out must be rows of ys' type")
-            _check_out(out, "out", addr, y, w, addr, plan.pos)
-        _abi.prism_expert_combine(plan.desc, _DT[y.dtype], C, y, plan.pos, w, addr, _ld(addr), out, _ld(out))
+    call = plan._call
+    key = ("combine", call, _sig(ys), _sig(weights), _sig(add), _sig(out))
+    p = _plans.get(key)
+    if p is None:
+        _sorted(ys, plan, None, None, "ys")
+        _weights(weights, plan)
+        C = ys.shape[1]
+        ld_add, ld_out = _by_token(add, plan, C, ys.dtype, "add"), _by_token(out, plan, C, ys.dtype, "out")
+        _need(ld_out is not None, "out's rows must lie evenly")
+        p = _keep(key, _Plan(call.desc, plan.device, ld_add is None or not ys.is_contiguous()
+                             or (weights is not None and not weights.is_contiguous())))
+        p.a = (_DT[ys.dtype], C, ld_add, ld_out)
+    if p.copy:
+        return expert_combine(ys.contiguous(), plan, None if weights is None else weights.contiguous(),
+                              add=_dense(add), out=out)
+    if not _current(p.index):
+        with torch.cuda.device(p.index):
+            return expert_combine(ys, plan, weights, add=add, out=out)
+    dt, C, ld_add, ld_out = p.a
+    if out is None:
+        out = torch.empty(plan.rows, C, dtype=ys.dtype, device=ys.device)
+    else:
+        _check_out(out, "out", add, ys, weights, plan._all)
+    _check("prism_expert_combine", _abi.lib().prism_expert_combine(
+        p.addr, dt, C, ys.data_ptr(), plan.pos.data_ptr(), _ptr(weights), _ptr(add), ld_add, out.data_ptr(), ld_out,
+        _stream(p.index)))
     return out
 
 
@@ -558,21 +739,41 @@ def expert_combine_backward(dout, ys, plan, weights=None, *, out=None, want_weig
     """(dys, dweights) of ``expert_combine``: dys[pos[t, j]] = weights[t, j] dout[t] and dweights[t, j] =
     ys[pos[t, j]] . dout[t] (0 where dropped; None with ``want_weights=False``, where ys may be None).  Rows of dys
     without a slot as in ``expert_dispatch``; ``out`` may be ys itself."""
-    d = _by_token(dout, plan, None, "dout")
-    C = d.shape[1]
-    w = _weights(weights, plan)
-    _need(ys is not None or not want_weights, "the weights' gradient needs ys")
-    y = None if ys is None or not want_weights else _sorted(ys, plan, C, dout.dtype, "ys").contiguous()
-    with _on(plan.device):
-        clear = out is None
-        if clear:
-            out = torch.empty((plan.rows_sorted, C), dtype=dout.dtype, device=plan.device)
-        else:
-            _need(_sorted(out, plan, C, dout.dtype, "out").is_contiguous(), "out must be dense")
-            _check_out(out, "out", y, d, y, w, plan.pos, plan.counts, plan.offsets)
-        dw = torch.empty((plan.rows, plan.top_k), dtype=torch.float32, device=plan.device) if want_weights else None
-        _abi.prism_expert_combine_bwd(plan.desc, _DT[dout.dtype], C, d, _ld(d), y, plan.pos, w, plan.counts,
-                                      plan.offsets, int(clear), out, dw)
+    if not want_weights:
+        ys = None
+    call = plan._call
+    key = ("dcombine", call, _sig(dout), _sig(ys), _sig(weights), _sig(out), want_weights)
+    p = _plans.get(key)
+    if p is None:
+        ld = _by_token(dout, plan, None, None, "dout")
+        C = dout.shape[1]
+        _weights(weights, plan)
+        _need(ys is not None or not want_weights, "the weights' gradient needs ys")
+        _sorted(ys, plan, C, dout.dtype, "ys")
+        _sorted(out, plan, C, dout.dtype, "out")
+        _need(out is None or out.is_contiguous(), "out must be dense")
+        p = _keep(key, _Plan(call.desc, plan.device, ld is None or (ys is not None and not ys.is_contiguous())
+                             or (weights is not None and not weights.is_contiguous())))
+        p.a = (_DT[dout.dtype], C, ld)
+    if p.copy:
+        return expert_combine_backward(_dense(dout), None if ys is None else ys.contiguous(), plan,
+                                       None if weights is None else weights.contiguous(), out=out,
+                                       want_weights=want_weights)
+    if not _current(p.index):
+        with torch.cuda.device(p.index):
+            return expert_combine_backward(dout, ys, plan, weights, out=out, want_weights=want_weights)
+    dt, C, ld = p.a
+    clear = out is None
+    if clear:
+        out = torch.empty(plan.rows_sorted, C, dtype=dout.dtype, device=dout.device)
+    else:
+        _check_out(out, "out", ys, dout, weights, plan._all)
+    dw = None
+    if want_weights:
+        dw = torch.empty(plan.rows, plan.top_k, dtype=torch.float32, device=dout.device)
+    _check("prism_expert_combine_bwd", _abi.lib().prism_expert_combine_bwd(
+        p.addr, dt, C, dout.data_ptr(), ld, _ptr(ys), plan.pos.data_ptr(), _ptr(weights), plan.counts.data_ptr(),
+        plan.offsets.data_ptr(), clear, out.data_ptr(), _ptr(dw), _stream(p.index)))
     return out, dw
 
 

@@ -184,10 +184,9 @@ def host(monkeypatch):
 
     def refuse(*a):
         raise AssertionError("the call was not refused")
-    for name in ("prism_block_norm_fwd", "prism_block_norm_bwd", "prism_head_rotate_fwd", "prism_head_rotate_bwd",
-                 "prism_expert_plan", "prism_expert_dispatch", "prism_expert_combine", "prism_expert_combine_bwd"):
-        monkeypatch.setattr(block._abi, name, refuse)
-    monkeypatch.setattr(block, "_on", lambda dev: block.contextlib.nullcontext())
+    monkeypatch.setattr(block, "_stream", refuse)
+    monkeypatch.setattr(block, "_current", lambda index: True)
+    monkeypatch.setattr(block, "_plans", {})
 
 
 def test_norm_tensor_checks(L, host):
