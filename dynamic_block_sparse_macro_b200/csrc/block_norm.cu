@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(512) k_block_norm_affine_join(const JoinArgs a
 }
 
 struct Split {
-    int64_t groups, per_group, seg_rows, segs;
+    int64_t groups, per_group, segs;
 };
 
 // Segments of rows, none across a group's end.  Where there are few groups, each is cut so that the
@@ -117,18 +117,16 @@ struct Split {
 // such teams, so that the last round's idle part is small.  No segment below four rows is cut:
 // its column sums cost as much as three rows.
 static Split split_rows(const prism_block_norm_t* n) {
-    Split s{0, 1, 1, 0};
+    Split s{0, 1, 0};
     if (n->rows == 0) return s;
     const int64_t rpg = n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
     s.groups = (n->rows + rpg - 1) / rpg;
-    const int threads = team_threads(n->channels) * cta_teams(n->channels);
-    const int64_t teams = (int64_t)kSMs * (threads <= 512 ? 512 / threads : 1) * cta_teams(n->channels);
+    const int64_t teams = (int64_t)kSMs * sm_teams(n->channels, bwd_ctas(team_bucket(team_threads(n->channels))));
     int64_t per = s.groups * 4 <= teams ? teams / s.groups : 8 * teams / s.groups;
     const int64_t most = (rpg + 3) / 4;
     if (per > most) per = most;
     if (per < 1) per = 1;
-    s.seg_rows = (rpg + per - 1) / per;
-    s.per_group = (rpg + s.seg_rows - 1) / s.seg_rows;
+    s.per_group = per;
     s.segs = s.groups * s.per_group;
     return s;
 }
@@ -257,7 +255,7 @@ extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, cons
     if (direct) { a.dgate = dgate; a.dscale = dscale; a.dshift = dshift; }
     a.R = n->rows;
     a.rpg = n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
-    a.seg_rows = s.seg_rows; a.segs = s.segs; a.per_group = (int)s.per_group;
+    a.segs = s.segs; a.per_group = (int)s.per_group;
     a.C = C; a.norm = n->norm; a.post = n->post_norm; a.eps = n->eps; a.res = n->res_scale;
     const int unit = unit_of(C, {has_y ? a.ld_z : 0, h ? a.ld_h : 0, dz ? a.ld_dz : 0, has_y ? a.ld_dy : 0, a.ld_dx,
                                  h ? a.ld_dh : 0, gate ? a.ld_gate : 0, scale ? a.ld_scale : 0},

@@ -13,6 +13,8 @@
 //   dscale_g = w ∘ A_g + b ∘ D_g,  dshift_g = D_g,  dgate_g = w_post ∘ B_g
 //   dw = sum_g (1 + scale_g) ∘ A_g,  db = sum_g (1 + scale_g) ∘ D_g,  dw_post = sum_g gate_g ∘ B_g
 //
+// A row's threads hold eight channels each.  A thread takes only channels of the row into a sum: what its
+// registers hold for places past the row's end is never used.
 // Everything between a load and a store is fp32: statistics, means and column sums too.  A result
 // that is stored as bf16 is rounded once, at its store; y comes from the unrounded z.
 #pragma once
@@ -42,7 +44,7 @@ struct BwdArgs {
     // direct: each group is one segment and its gradients are written by the row kernel
     float *dgate, *dscale, *dshift;
     float* part;                       // [segments][3][C] column sums A, D, B; null: not wanted
-    int64_t R, rpg, seg_rows, segs;    // segs = groups x segments a group
+    int64_t R, rpg, segs;              // segs = groups x segments a group
     int64_t ld_z, ld_h, ld_dz, ld_dy, ld_dx, ld_dh, ld_gate, ld_scale;
     int C, norm, post, per_group;
     float eps, res;
@@ -76,17 +78,23 @@ template <int E> __device__ __forceinline__ void store_vec(float* p, const float
     }
 }
 
-template <typename TX, typename TH, int E, int MAXT, bool HAS_H>
-__global__ void __launch_bounds__(MAXT) k_block_norm_fwd(const FwdArgs a) {
+template <typename TX, typename TH, int E, int MAXT, bool HAS_H, int CTAS>
+__global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fwd(const FwdArgs a) {
     constexpr int U = 8 / E;
-    __shared__ float4 sums[8][64];
-    Team team;
-    team.init(&sums[0][0]);
+    __shared__ float4 sums[Team<MAXT>::kBufs];
+    Team<MAXT> team;
+    team.init(sums);
     const int t = threadIdx.x, T = blockDim.x, C = a.C;
-    const int64_t nteams = (int64_t)gridDim.x * blockDim.y, me = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int64_t r0 = a.R * me / nteams, r1 = a.R * (me + 1) / nteams;
+    // of a CTA-wide team the compiler sees that its row is the same for all threads
+    const int64_t nteams = MAXT == 32 ? (int64_t)gridDim.x * blockDim.y : gridDim.x;
+    const int64_t me = MAXT == 32 ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
+    // All teams move over the rows together where groups are long, else each over rows of its own, whose vectors it
+    // then loads once a group.
+    const bool together = a.rpg >= 4 * nteams;
+    const int64_t r0 = together ? me : a.R * me / nteams, r1 = together ? a.R : a.R * (me + 1) / nteams;
+    const int64_t step = together ? nteams : 1;
     if (r0 >= r1) return;
-    const float inv_c = 1.f / (float)C;
+    const float fc = (float)C, inv_c = 1.f / fc;
     const TX* x = (const TX*)a.x;
     const TH* h = (const TH*)a.h;
 
@@ -141,10 +149,10 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_fwd(const FwdArgs a) {
             }
         }
     };
-    int64_t g = r0 / a.rpg, left = (g + 1) * a.rpg - r0;
+    int64_t g = r0 / a.rpg, next = (g + 1) * a.rpg;
     vectors(g);
 
-    for (int64_t r = r0; r < r1; ++r) {
+    for (int64_t r = r0; r < r1; r += step) {
         float v[U * E];
 #pragma unroll
         for (int i = 0; i < U * E; ++i) v[i] = 0.f;
@@ -159,12 +167,11 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_fwd(const FwdArgs a) {
             for (int u = 0; u < U; ++u)
                 if ((u * T + t) * E < C) unpack<E>(rh[u], hv + u * E);
         }
-        if (r + 1 < r1) fetch(r + 1);
-        if (left == 0) {
+        if (r + step < r1) fetch(r + step);
+        if (r >= next) {                  // steps are shorter than groups
             vectors(++g);
-            left = a.rpg;
+            next += a.rpg;
         }
-        --left;
 
         // mean (layer) and 1/std of the row held in f; f becomes f - mean
         auto stats = [&](float* f, int kind) {
@@ -172,7 +179,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_fwd(const FwdArgs a) {
                 float s = 0.f;
 #pragma unroll
                 for (int i = 0; i < U * E; ++i) s += f[i];
-                const float m = team.sum1(s) / (float)C;
+                const float m = mean_of(team.sum1(s), fc, inv_c);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if ((u * T + t) * E < C) {
@@ -187,13 +194,17 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_fwd(const FwdArgs a) {
         };
 
         if constexpr (HAS_H) {
-            const float rh_ = a.post != PRISM_NORM_NONE ? stats(hv, a.post) : 1.f;
+            if (a.post != PRISM_NORM_NONE) {
+                const float rh_ = stats(hv, a.post);
 #pragma unroll
-            for (int i = 0; i < U * E; ++i) v[i] = fmaf(gate[i], hv[i] * rh_, a.res * v[i]);
+                for (int i = 0; i < U * E; ++i) hv[i] *= rh_;
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int c = (u * T + t) * E;
                 if (c < C) {
+#pragma unroll
+                    for (int i = u * E; i < u * E + E; ++i) v[i] = fmaf(a.res, v[i], gate[i] * hv[i]);
                     Pack<TX, E> o;
                     pack<E>(o, v + u * E);
                     store((TX*)a.z + r * a.ld_z + c, o);
@@ -218,21 +229,21 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_fwd(const FwdArgs a) {
     }
 }
 
-template <typename TX, typename TH, int E, int MAXT, bool HAS_H>
-__global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
+template <typename TX, typename TH, int E, int MAXT, bool HAS_H, int CTAS>
+__global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bwd(const BwdArgs a) {
     constexpr int U = 8 / E;
-    __shared__ float4 sums[8][64];
-    Team team;
-    team.init(&sums[0][0]);
+    __shared__ float4 sums[Team<MAXT>::kBufs];
+    Team<MAXT> team;
+    team.init(sums);
     const int t = threadIdx.x, T = blockDim.x, C = a.C;
-    const int64_t seg = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t seg = MAXT == 32 ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
     if (seg >= a.segs) return;
     const int64_t g = seg / a.per_group;
-    const int64_t r0 = g * a.rpg + (seg - g * a.per_group) * a.seg_rows;
-    int64_t r1 = r0 + a.seg_rows;
-    if (r1 > (g + 1) * a.rpg) r1 = (g + 1) * a.rpg;
+    // segment s of a group takes its rows s, s + per_group, ...: all teams move over the rows together
+    const int64_t r0 = g * a.rpg + (seg - g * a.per_group), step = a.per_group;
+    int64_t r1 = (g + 1) * a.rpg;
     if (r1 > a.R) r1 = a.R;
-    const float inv_c = 1.f / (float)C;
+    const float fc = (float)C, inv_c = 1.f / fc;
     const bool has_y = a.norm != PRISM_NORM_NONE;
 
     Pack<TX, E> rz[U], rdz[U];
@@ -262,7 +273,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
         for (int e = 0; e < E; ++e) mul[u * E + e] = 1.f;
         if constexpr (HAS_H) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) gate[u * E + e] = c < C ? 1.f : 0.f;   // what lies past the row adds nothing
+            for (int e = 0; e < E; ++e) gate[u * E + e] = 1.f;
         }
         if (c >= C) continue;
         if (a.w) load_vec<E>(mul + u * E, a.w + c);
@@ -289,7 +300,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
         for (int i = 0; i < U * E; ++i) sB[i] = 0.f;
     }
 
-    for (int64_t r = r0; r < r1; ++r) {
+    for (int64_t r = r0; r < r1; r += step) {
         float z[U * E], dy[U * E], d[U * E], h[HAS_H ? U * E : 1];
 #pragma unroll
         for (int i = 0; i < U * E; ++i) z[i] = dy[i] = d[i] = 0.f;
@@ -309,21 +320,25 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
             for (int u = 0; u < U; ++u)
                 if ((u * T + t) * E < C) unpack<E>(rh[u], h + u * E);
         }
-        if (r + 1 < r1) fetch(r + 1);
+        if (r + step < r1) fetch(r + step);
 
         // means first (layer): of z, of c = dy ∘ mul and of h
         float mc = 0.f;
         if (a.norm == PRISM_NORM_LAYER || (HAS_H && a.post == PRISM_NORM_LAYER)) {
             float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < U * E; ++i) {
-                s[0] += z[i];
-                s[1] = fmaf(dy[i], mul[i], s[1]);
-                if constexpr (HAS_H) s[2] += h[i];
-            }
+            for (int u = 0; u < U; ++u)
+                if ((u * T + t) * E < C) {
+#pragma unroll
+                    for (int i = u * E; i < u * E + E; ++i) {
+                        s[0] += z[i];
+                        s[1] = fmaf(dy[i], mul[i], s[1]);
+                        if constexpr (HAS_H) s[2] += h[i];
+                    }
+                }
             team.sum(s);
-            const float mz = a.norm == PRISM_NORM_LAYER ? s[0] / (float)C : 0.f;
-            const float mh = a.post == PRISM_NORM_LAYER ? s[2] / (float)C : 0.f;
+            const float mz = a.norm == PRISM_NORM_LAYER ? mean_of(s[0], fc, inv_c) : 0.f;
+            const float mh = a.post == PRISM_NORM_LAYER ? mean_of(s[2], fc, inv_c) : 0.f;
             mc = a.norm == PRISM_NORM_LAYER ? s[1] * inv_c : 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -340,21 +355,30 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
         if (has_y || (HAS_H && a.post != PRISM_NORM_NONE)) {
             float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < U * E; ++i) {
-                s[0] = fmaf(z[i], z[i], s[0]);
-                s[1] = fmaf(dy[i] * mul[i], z[i], s[1]);
-                if constexpr (HAS_H) s[2] = fmaf(h[i], h[i], s[2]);
-            }
+            for (int u = 0; u < U; ++u)
+                if ((u * T + t) * E < C) {
+#pragma unroll
+                    for (int i = u * E; i < u * E + E; ++i) {
+                        s[0] = fmaf(z[i], z[i], s[0]);
+                        s[1] = fmaf(dy[i] * mul[i], z[i], s[1]);
+                        if constexpr (HAS_H) s[2] = fmaf(h[i], h[i], s[2]);
+                    }
+                }
             team.sum(s);
             if (has_y) {
                 const float rs = rsqrtf(s[0] * inv_c + a.eps), mcn = s[1] * rs * inv_c;
 #pragma unroll
-                for (int i = 0; i < U * E; ++i) {
-                    const float n = z[i] * rs;
-                    sA[i] = fmaf(dy[i], n, sA[i]);
-                    sD[i] += dy[i];
-                    d[i] = fmaf(rs, fmaf(dy[i], mul[i], -mc) - n * mcn, d[i]);
-                }
+                for (int u = 0; u < U; ++u)
+                    if ((u * T + t) * E < C) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const int i = u * E + e;
+                            const float n = z[i] * rs;
+                            sA[i] = fmaf(dy[i], n, sA[i]);
+                            sD[i] += dy[i];
+                            d[i] = fmaf(rs, fmaf(dy[i], mul[i], -mc) - n * mcn, d[i]);
+                        }
+                    }
             }
             if (HAS_H && a.post != PRISM_NORM_NONE) rh_ = rsqrtf(s[2] * inv_c + a.eps);
         }
@@ -374,13 +398,17 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
         if constexpr (HAS_H) {
             float s[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < U * E; ++i) {
-                h[i] *= rh_;
-                sB[i] = fmaf(d[i], h[i], sB[i]);
-                d[i] *= gate[i];
-                s[0] += d[i];
-                s[1] = fmaf(d[i], h[i], s[1]);
-            }
+            for (int u = 0; u < U; ++u)
+                if ((u * T + t) * E < C) {
+#pragma unroll
+                    for (int i = u * E; i < u * E + E; ++i) {
+                        h[i] *= rh_;
+                        sB[i] = fmaf(d[i], h[i], sB[i]);
+                        d[i] *= gate[i];
+                        s[0] += d[i];
+                        s[1] = fmaf(d[i], h[i], s[1]);
+                    }
+                }
             float md = 0.f, mdn = 0.f;
             if (a.post != PRISM_NORM_NONE) {
                 team.sum(s);
@@ -437,46 +465,65 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
     }
 }
 
-// threads of a team: 8 channels a thread, a whole number of warps
-inline int team_threads(int C) { return ((C + 7) / 8 + 31) / 32 * 32; }
-// teams of a CTA: CTAs of about 256 threads
+// threads of a team: 8 channels a thread; 8, 16 or a whole number of warps
+inline int team_threads(int C) {
+    const int n = (C + 7) / 8;
+    return n <= 8 ? 8 : n <= 16 ? 16 : (n + 31) / 32 * 32;
+}
+// teams of a CTA: one, or 256 threads of teams within a warp
 inline int cta_teams(int C) {
-    const int n = 256 / team_threads(C);
-    return n < 1 ? 1 : n;
+    const int t = team_threads(C);
+    return t <= 32 ? 256 / t : 1;
+}
+// the kernel's MAXT for a team, and the CTAs of at most that many threads that its registers leave room for on an SM
+constexpr int team_bucket(int threads) {
+    return threads <= 32 ? 32 : threads <= 256 ? 256 : threads <= 384 ? 384 : threads <= 512 ? 512 : threads <= 768 ? 768 : 1024;
+}
+constexpr int fwd_ctas(int maxt) { return maxt <= 256 ? 3 : maxt <= 384 ? 2 : 1; }
+constexpr int bwd_ctas(int maxt) { return maxt <= 256 ? 2 : 1; }
+// teams that run at a time on an SM
+inline int sm_teams(int C, int ctas) {
+    const int t = team_threads(C), most = team_bucket(t) == 32 ? 256 : team_bucket(t);
+    return ctas * most / t;
 }
 
 // one launcher a pair of types (stream, branch); unit = channels an access
 template <typename TX, typename TH> void launch_fwd(const FwdArgs& a, int unit, cudaStream_t s);
 template <typename TX, typename TH> void launch_bwd(const BwdArgs& a, int unit, cudaStream_t s);
 
-#define PRISM_BN_BY_SIZE(KERNEL, TX, TH, E, H, GRID, BLOCK, A, S)                      \
-    do {                                                                              \
-        const int threads_ = (BLOCK).x * (BLOCK).y;                                   \
-        if (threads_ <= 256) KERNEL<TX, TH, E, 256, H><<<GRID, BLOCK, 0, S>>>(A);     \
-        else if (threads_ <= 512) KERNEL<TX, TH, E, 512, H><<<GRID, BLOCK, 0, S>>>(A); \
-        else KERNEL<TX, TH, E, 1024, H><<<GRID, BLOCK, 0, S>>>(A);                    \
+#define PRISM_BN_BY_SIZE(KERNEL, CTAS, TX, TH, E, H)                                                     \
+    do {                                                                                                \
+        switch (team_bucket(block.x)) {                                                                 \
+            case 32: KERNEL<TX, TH, E, 32, H, CTAS(32)><<<grid, block, 0, s>>>(a); break;               \
+            case 256: KERNEL<TX, TH, E, 256, H, CTAS(256)><<<grid, block, 0, s>>>(a); break;            \
+            case 384: KERNEL<TX, TH, E, 384, H, CTAS(384)><<<grid, block, 0, s>>>(a); break;            \
+            case 512: KERNEL<TX, TH, E, 512, H, CTAS(512)><<<grid, block, 0, s>>>(a); break;            \
+            case 768: KERNEL<TX, TH, E, 768, H, CTAS(768)><<<grid, block, 0, s>>>(a); break;            \
+            default: KERNEL<TX, TH, E, 1024, H, CTAS(1024)><<<grid, block, 0, s>>>(a); break;           \
+        }                                                                                               \
     } while (0)
 
-#define PRISM_BN_BY_UNIT(KERNEL, TX, TH, H, GRID, BLOCK, A, UNIT, S)                  \
+#define PRISM_BN_BY_UNIT(KERNEL, CTAS, TX, TH, H)                                      \
     do {                                                                              \
-        if ((UNIT) == 8) PRISM_BN_BY_SIZE(KERNEL, TX, TH, 8, H, GRID, BLOCK, A, S);   \
-        else if ((UNIT) == 2) PRISM_BN_BY_SIZE(KERNEL, TX, TH, 2, H, GRID, BLOCK, A, S); \
-        else PRISM_BN_BY_SIZE(KERNEL, TX, TH, 1, H, GRID, BLOCK, A, S);               \
+        if (unit == 8) PRISM_BN_BY_SIZE(KERNEL, CTAS, TX, TH, 8, H);                  \
+        else if (unit == 2) PRISM_BN_BY_SIZE(KERNEL, CTAS, TX, TH, 2, H);             \
+        else PRISM_BN_BY_SIZE(KERNEL, CTAS, TX, TH, 1, H);                            \
     } while (0)
 
 #define PRISM_BN_INSTANTIATE(TX, TH)                                                                   \
     template <> void launch_fwd<TX, TH>(const FwdArgs& a, int unit, cudaStream_t s) {                  \
         const dim3 block(team_threads(a.C), cta_teams(a.C));                                           \
-        const int64_t want = (a.R + block.y - 1) / block.y, most = kSMs * (int64_t)(1024 / (block.x * block.y) > 0 ? 1024 / (block.x * block.y) : 1); \
+        const int64_t want = (a.R + block.y - 1) / block.y;                                            \
+        const int64_t most = kSMs * (int64_t)sm_teams(a.C, fwd_ctas(team_bucket(block.x))) / block.y;  \
         const dim3 grid((unsigned)(want < most ? want : most));                                        \
-        if (a.h) PRISM_BN_BY_UNIT(k_block_norm_fwd, TX, TH, true, grid, block, a, unit, s);            \
-        else PRISM_BN_BY_UNIT(k_block_norm_fwd, TX, TH, false, grid, block, a, unit, s);               \
+        if (a.h) PRISM_BN_BY_UNIT(k_block_norm_fwd, fwd_ctas, TX, TH, true);                           \
+        else PRISM_BN_BY_UNIT(k_block_norm_fwd, fwd_ctas, TX, TH, false);                              \
     }                                                                                                  \
     template <> void launch_bwd<TX, TH>(const BwdArgs& a, int unit, cudaStream_t s) {                  \
         const dim3 block(team_threads(a.C), cta_teams(a.C));                                           \
         const dim3 grid((unsigned)((a.segs + block.y - 1) / block.y));                                 \
-        if (a.h) PRISM_BN_BY_UNIT(k_block_norm_bwd, TX, TH, true, grid, block, a, unit, s);            \
-        else PRISM_BN_BY_UNIT(k_block_norm_bwd, TX, TH, false, grid, block, a, unit, s);               \
+        if (a.h) PRISM_BN_BY_UNIT(k_block_norm_bwd, bwd_ctas, TX, TH, true);                           \
+        else PRISM_BN_BY_UNIT(k_block_norm_bwd, bwd_ctas, TX, TH, false);                              \
     }
 
 }  // namespace bn

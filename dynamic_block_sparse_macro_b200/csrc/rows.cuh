@@ -90,41 +90,63 @@ template <int N> __device__ __forceinline__ void pack(Pack<__nv_bfloat16, N>& p,
     }
 }
 
-// The threads that share a row: a whole number of warps, threadIdx.x within
-// the team and threadIdx.y its number in the CTA.  A sum over several warps
-// goes through shared memory with one named barrier (id team + 1): two
-// buffers alternate, and a thread can write a buffer again only after the
-// barrier of the sum in between, which every thread reaches after it has read.
-struct Team {
-    float4* buf;       // [2][32] of this team
-    int threads, id, flip;
+// s / c, where 1 / c is at hand: one correction makes it exact where the quotient is
+__device__ __forceinline__ float mean_of(float s, float c, float inv_c) {
+    const float m = s * inv_c;
+    return fmaf(fmaf(-m, c, s), inv_c, m);
+}
+
+// The threads that share a row: 8, 16 or 32 lanes (MAXT = 32; threadIdx.x within the team, threadIdx.y its number
+// in the CTA), or a whole CTA of up to MAXT threads, a multiple of 32.  A sum over a CTA's warps goes through shared
+// memory with one barrier: two buffers alternate, and a thread can write a buffer again only after the barrier of
+// the sum in between, which every thread reaches after it has read.  (Teams of several warps in one CTA, each with a
+// named barrier, took 30% longer.)
+template <int MAXT> struct Team {
+    static constexpr int W = MAXT <= 256 ? 8 : MAXT <= 512 ? 16 : 32;   // warps of a team at most
+    static constexpr int kBufs = MAXT == 32 ? 1 : 2 * W;
+    float4* buf;       // [2][W]
+    uint32_t mask;     // of the team's lanes in a warp
+    int flip;
 
     __device__ __forceinline__ void init(float4* smem) {
-        threads = blockDim.x;
-        id = threadIdx.y;
-        buf = smem + id * 64;
+        buf = smem;
         flip = 0;
+        mask = 0xffffffffu;
+        if (MAXT == 32 && blockDim.x < 32) {
+            const int lane = (threadIdx.y * blockDim.x + threadIdx.x) & 31;
+            mask = ((1u << blockDim.x) - 1) << (lane & ~(blockDim.x - 1));
+        }
     }
     // sums of up to four values over the team, in a fixed order
     template <int N> __device__ __forceinline__ void sum(float (&v)[N]) {
         static_assert(N <= 4, "four values");
+        if constexpr (MAXT == 32) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-        if (threads == 32) return;
-        float* p = reinterpret_cast<float*>(buf + flip * 32);
-        flip ^= 1;
-        const int l = threadIdx.x & 31;
-        if (l == 0) {
+            for (int o = 16; o > 0; o >>= 1)
+                if (o < blockDim.x) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) p[4 * (threadIdx.x >> 5) + i] = v[i];
+                    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(mask, v[i], o);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+            float4* b = buf + flip * W;
+            flip ^= 1;
+            const int l = threadIdx.x & 31, i = l & (W - 1);
+            if (l == 0)
+                b[threadIdx.x >> 5] = make_float4(v[0], N > 1 ? v[N > 1 ? 1 : 0] : 0.f, N > 2 ? v[N > 2 ? 2 : 0] : 0.f,
+                                                  N > 3 ? v[N > 3 ? 3 : 0] : 0.f);
+            __syncthreads();
+            const float4 q = i < (blockDim.x >> 5) ? b[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[0] = q.x;
+            if constexpr (N > 1) v[1] = q.y;
+            if constexpr (N > 2) v[2] = q.z;
+            if constexpr (N > 3) v[3] = q.w;
+#pragma unroll
+            for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
         }
-        // a row that ends inside a warp can leave the warp's lanes apart here: all of them, the storing one too,
-        // meet before the barrier counts the warp
-        __syncwarp();
-        asm volatile("barrier.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
-        const bool in = l < (threads >> 5);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(in ? p[4 * l + i] : 0.f);
     }
     __device__ __forceinline__ float sum1(float a) {
         float v[1] = {a};
