@@ -9,12 +9,12 @@ namespace bn {
 
 constexpr int kMaxJoin = 64;
 
-template <> void launch_fwd<float, float>(const FwdArgs&, int, cudaStream_t);
-template <> void launch_fwd<float, __nv_bfloat16>(const FwdArgs&, int, cudaStream_t);
-template <> void launch_fwd<__nv_bfloat16, __nv_bfloat16>(const FwdArgs&, int, cudaStream_t);
-template <> void launch_bwd<float, float>(const BwdArgs&, int, cudaStream_t);
-template <> void launch_bwd<float, __nv_bfloat16>(const BwdArgs&, int, cudaStream_t);
-template <> void launch_bwd<__nv_bfloat16, __nv_bfloat16>(const BwdArgs&, int, cudaStream_t);
+template <> prism_status_t launch_fwd<float, float>(const FwdArgs&, int, cudaStream_t);
+template <> prism_status_t launch_fwd<float, __nv_bfloat16>(const FwdArgs&, int, cudaStream_t);
+template <> prism_status_t launch_fwd<__nv_bfloat16, __nv_bfloat16>(const FwdArgs&, int, cudaStream_t);
+template <> prism_status_t launch_bwd<float, float>(const BwdArgs&, int, cudaStream_t);
+template <> prism_status_t launch_bwd<float, __nv_bfloat16>(const BwdArgs&, int, cudaStream_t);
+template <> prism_status_t launch_bwd<__nv_bfloat16, __nv_bfloat16>(const BwdArgs&, int, cudaStream_t);
 
 struct JoinArgs {
     const float* part;                  // [segments][3][C]
@@ -203,10 +203,10 @@ extern "C" prism_status_t prism_block_norm_fwd(const prism_block_norm_t* n, cons
     const int unit = unit_of(C, {a.ld_x, h ? a.ld_h : 0, h ? a.ld_z : 0, has_y ? a.ld_y : 0, gate ? a.ld_gate : 0,
                                  scale ? a.ld_scale : 0, shift ? a.ld_shift : 0},
                              {x, h, gate, w_post, w, b, scale, shift, z, y});
-    if (n->stream_dtype == PRISM_BF16) launch_fwd<__nv_bfloat16, __nv_bfloat16>(a, unit, stream);
-    else if (n->branch_dtype == PRISM_BF16) launch_fwd<float, __nv_bfloat16>(a, unit, stream);
-    else launch_fwd<float, float>(a, unit, stream);
-    return launch_status(1);
+    if (n->stream_dtype == PRISM_BF16) st = launch_fwd<__nv_bfloat16, __nv_bfloat16>(a, unit, stream);
+    else if (n->branch_dtype == PRISM_BF16) st = launch_fwd<float, __nv_bfloat16>(a, unit, stream);
+    else st = launch_fwd<float, float>(a, unit, stream);
+    return st == PRISM_OK ? launch_status(1) : st;
 }
 
 extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, const void* z, const void* h,
@@ -261,9 +261,10 @@ extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, cons
                                  h ? a.ld_dh : 0, gate ? a.ld_gate : 0, scale ? a.ld_scale : 0},
                              {has_y ? z : nullptr, h, gate, w_post, w, b, scale, dz, dy, dx, dh, dgate, dscale, dshift,
                               part ? ws : nullptr});
-    if (n->stream_dtype == PRISM_BF16) launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, unit, stream);
-    else if (n->branch_dtype == PRISM_BF16) launch_bwd<float, __nv_bfloat16>(a, unit, stream);
-    else launch_bwd<float, float>(a, unit, stream);
+    if (n->stream_dtype == PRISM_BF16) st = launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, unit, stream);
+    else if (n->branch_dtype == PRISM_BF16) st = launch_bwd<float, __nv_bfloat16>(a, unit, stream);
+    else st = launch_bwd<float, float>(a, unit, stream);
+    if (st != PRISM_OK) return st;
     int launches = 1;
     JoinArgs j{(const float*)ws, w, b, w_post, scale, gate, dgate, dscale, dshift, dw, db, dw_post,
                (float*)ws + s.segs * 3 * C, s.groups, s.segs, a.ld_scale, a.ld_gate, C, (int)s.per_group};

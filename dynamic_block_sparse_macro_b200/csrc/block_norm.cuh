@@ -19,6 +19,8 @@
 // that is stored as bf16 is rounded once, at its store; y comes from the unrounded z.
 #pragma once
 
+#include <type_traits>
+
 #include "rows.cuh"
 
 namespace prism {
@@ -81,7 +83,7 @@ template <int E> __device__ __forceinline__ void store_vec(float* p, const float
 template <typename TX, typename TH, int E, int MAXT, bool HAS_H, int CTAS>
 __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fwd(const FwdArgs a) {
     constexpr int U = 8 / E;
-    __shared__ float4 sums[Team<MAXT>::kBufs];
+    __shared__ float sums[Team<MAXT>::kFloats];
     Team<MAXT> team;
     team.init(sums);
     const int t = threadIdx.x, T = blockDim.x, C = a.C;
@@ -229,10 +231,21 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fw
     }
 }
 
-template <typename TX, typename TH, int E, int MAXT, bool HAS_H, int CTAS>
+// Rows on their way to a team's threads: through shared memory, D rows ahead (Lane), or, for elements of two bytes
+// that lie on no wider boundary, through registers, one row ahead.
+extern __shared__ __align__(16) char g_ring[];
+
+// What the backward's branch is: none, one that goes to the sum as it is, or one with a norm of its own.
+enum Branch { kNoBranch = 0, kPlain = 1, kNormed = 2 };
+
+template <typename TX, typename TH, int E, int MAXT, int BR, int CTAS, int D>
 __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bwd(const BwdArgs a) {
     constexpr int U = 8 / E;
-    __shared__ float4 sums[Team<MAXT>::kBufs];
+    constexpr bool HAS_H = BR != kNoBranch;
+    constexpr bool RING = Lane<TX, E>::kAsync && Lane<TH, E>::kAsync;
+    using LX = Lane<TX, E>;
+    using LH = Lane<TH, E>;
+    __shared__ float sums[Team<MAXT>::kFloats];
     Team<MAXT> team;
     team.init(sums);
     const int t = threadIdx.x, T = blockDim.x, C = a.C;
@@ -245,200 +258,257 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
     if (r1 > a.R) r1 = a.R;
     const float fc = (float)C, inv_c = 1.f / fc;
     const bool has_y = a.norm != PRISM_NORM_NONE;
+    auto in = [&](int i) { return ((i / E) * T + t) * E < C; };          // whether channel i of the thread's eight is the row's
+    // the means that belong to pair i: 0 past the row's end, where everything stays 0
+    auto pair = [&](float m, int i) { return f2(in(2 * i) ? m : 0.f, in(2 * i + 1) ? m : 0.f); };
 
-    Pack<TX, E> rz[U], rdz[U];
-    Pack<TH, E> rh[U], rdy[U];
-    auto fetch = [&](int64_t r) {
+    // a stage: z, dz (TX), then dy, h (TH)
+    const int threads = MAXT == 32 ? 256 : T, tid = MAXT == 32 ? threadIdx.y * T + t : t;
+    const uint32_t ring = RING ? (uint32_t)__cvta_generic_to_shared(g_ring) : 0u;
+    const int o_dz = LX::kBytes * threads, o_dy = 2 * LX::kBytes * threads, o_h = o_dy + LH::kBytes * threads;
+    const int stage_bytes = (2 * LX::kBytes + (HAS_H ? 2 : 1) * LH::kBytes) * threads;
+    Pack<TX, E> rz[RING ? 1 : U], rdz[RING ? 1 : U];
+    Pack<TH, E> rh[RING ? 1 : U], rdy[RING ? 1 : U];
+    if constexpr (RING) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = (u * T + t) * E;
-            if (c < C) {
+        for (int i = 0; i < D; ++i) {
+            char* s = g_ring + i * stage_bytes;
+            LX::clear(s, threads, tid, t, T, C, !has_y);
+            LH::clear(s + o_dy, threads, tid, t, T, C, !has_y);
+            LX::clear(s + o_dz, threads, tid, t, T, C, !a.dz);
+            if constexpr (HAS_H) LH::clear(s + o_h, threads, tid, t, T, C, false);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) rz[u].w[0] = rdz[u].w[0] = rh[u].w[0] = rdy[u].w[0] = 0u;   // E = 1
+    }
+    auto fetch = [&](int64_t r, int stage) {
+        if constexpr (RING) {
+            if (r < r1) {
+                const uint32_t s = ring + stage * stage_bytes;
                 if (has_y) {
-                    load(rz[u], (const TX*)a.z + r * a.ld_z + c);
-                    load(rdy[u], (const TH*)a.dy + r * a.ld_dy + c);
+                    LX::fetch(s, threads, tid, (const TX*)a.z + r * a.ld_z, t, T, C);
+                    LH::fetch(s + o_dy, threads, tid, (const TH*)a.dy + r * a.ld_dy, t, T, C);
                 }
-                if (a.dz) load(rdz[u], (const TX*)a.dz + r * a.ld_dz + c);
-                if (HAS_H) load(rh[u], (const TH*)a.h + r * a.ld_h + c);
+                if (a.dz) LX::fetch(s + o_dz, threads, tid, (const TX*)a.dz + r * a.ld_dz, t, T, C);
+                if constexpr (HAS_H) LH::fetch(s + o_h, threads, tid, (const TH*)a.h + r * a.ld_h, t, T, C);
+            }
+            cp_commit();
+        } else if (r < r1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (u * T + t) * E;
+                if (c < C) {
+                    if (has_y) {
+                        load(rz[u], (const TX*)a.z + r * a.ld_z + c);
+                        load(rdy[u], (const TH*)a.dy + r * a.ld_dy + c);
+                    }
+                    if (a.dz) load(rdz[u], (const TX*)a.dz + r * a.ld_dz + c);
+                    if (HAS_H) load(rh[u], (const TH*)a.h + r * a.ld_h + c);
+                }
             }
         }
     };
-    if (r0 < r1) fetch(r0);
+#pragma unroll
+    for (int i = 0; i < (RING ? D : 1); ++i) fetch(r0 + i * step, i);
 
-    float mul[U * E], gate[HAS_H ? U * E : 1];
+    F2 mul[4], gate[HAS_H ? 4 : 1];
+    {
+        float m[8], q[8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = (u * T + t) * E;
-        float s[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) mul[u * E + e] = 1.f;
-        if constexpr (HAS_H) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) gate[u * E + e] = 1.f;
-        }
-        if (c >= C) continue;
-        if (a.w) load_vec<E>(mul + u * E, a.w + c);
-        if (a.scale) {
-            load_vec<E>(s, a.scale + g * a.ld_scale + c);
-#pragma unroll
-            for (int e = 0; e < E; ++e) mul[u * E + e] *= 1.f + s[e];
-        }
-        if constexpr (HAS_H) {
-            if (a.gate) load_vec<E>(gate + u * E, a.gate + g * a.ld_gate + c);
-            if (a.w_post) {
-                load_vec<E>(s, a.w_post + c);
-#pragma unroll
-                for (int e = 0; e < E; ++e) gate[u * E + e] *= s[e];
-            }
-        }
-    }
-
-    float sA[U * E], sD[U * E], sB[HAS_H ? U * E : 1];
-#pragma unroll
-    for (int i = 0; i < U * E; ++i) sA[i] = sD[i] = 0.f;
-    if constexpr (HAS_H) {
-#pragma unroll
-        for (int i = 0; i < U * E; ++i) sB[i] = 0.f;
-    }
-
-    for (int64_t r = r0; r < r1; r += step) {
-        float z[U * E], dy[U * E], d[U * E], h[HAS_H ? U * E : 1];
-#pragma unroll
-        for (int i = 0; i < U * E; ++i) z[i] = dy[i] = d[i] = 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if ((u * T + t) * E < C) {
-                if (has_y) {
-                    unpack<E>(rz[u], z + u * E);
-                    unpack<E>(rdy[u], dy + u * E);
-                }
-                if (a.dz) unpack<E>(rdz[u], d + u * E);
-            }
-        if constexpr (HAS_H) {
-#pragma unroll
-            for (int i = 0; i < U * E; ++i) h[i] = 0.f;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((u * T + t) * E < C) unpack<E>(rh[u], h + u * E);
-        }
-        if (r + step < r1) fetch(r + step);
-
-        // means first (layer): of z, of c = dy ∘ mul and of h
-        float mc = 0.f;
-        if (a.norm == PRISM_NORM_LAYER || (HAS_H && a.post == PRISM_NORM_LAYER)) {
-            float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((u * T + t) * E < C) {
-#pragma unroll
-                    for (int i = u * E; i < u * E + E; ++i) {
-                        s[0] += z[i];
-                        s[1] = fmaf(dy[i], mul[i], s[1]);
-                        if constexpr (HAS_H) s[2] += h[i];
-                    }
-                }
-            team.sum(s);
-            const float mz = a.norm == PRISM_NORM_LAYER ? mean_of(s[0], fc, inv_c) : 0.f;
-            const float mh = a.post == PRISM_NORM_LAYER ? mean_of(s[2], fc, inv_c) : 0.f;
-            mc = a.norm == PRISM_NORM_LAYER ? s[1] * inv_c : 0.f;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((u * T + t) * E < C) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        z[u * E + e] -= mz;
-                        if constexpr (HAS_H) h[u * E + e] -= mh;
-                    }
-                }
-        }
-        // second moments, and c against z
-        float rh_ = 1.f;
-        if (has_y || (HAS_H && a.post != PRISM_NORM_NONE)) {
-            float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((u * T + t) * E < C) {
-#pragma unroll
-                    for (int i = u * E; i < u * E + E; ++i) {
-                        s[0] = fmaf(z[i], z[i], s[0]);
-                        s[1] = fmaf(dy[i] * mul[i], z[i], s[1]);
-                        if constexpr (HAS_H) s[2] = fmaf(h[i], h[i], s[2]);
-                    }
-                }
-            team.sum(s);
-            if (has_y) {
-                const float rs = rsqrtf(s[0] * inv_c + a.eps), mcn = s[1] * rs * inv_c;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if ((u * T + t) * E < C) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const int i = u * E + e;
-                            const float n = z[i] * rs;
-                            sA[i] = fmaf(dy[i], n, sA[i]);
-                            sD[i] += dy[i];
-                            d[i] = fmaf(rs, fmaf(dy[i], mul[i], -mc) - n * mcn, d[i]);
-                        }
-                    }
-            }
-            if (HAS_H && a.post != PRISM_NORM_NONE) rh_ = rsqrtf(s[2] * inv_c + a.eps);
-        }
-        const float res = HAS_H ? a.res : 1.f;
+        for (int i = 0; i < 8; ++i) m[i] = q[i] = 1.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = (u * T + t) * E;
+            float s[E];
             if (c < C) {
-                float o[E];
+                if (a.w) load_vec<E>(m + u * E, a.w + c);
+                if (a.scale) {
+                    load_vec<E>(s, a.scale + g * a.ld_scale + c);
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = res * d[u * E + e];
-                Pack<TX, E> p;
-                pack<E>(p, o);
-                store((TX*)a.dx + r * a.ld_dx + c, p);
-            }
-        }
-        if constexpr (HAS_H) {
-            float s[2] = {0.f, 0.f};
+                    for (int e = 0; e < E; ++e) m[u * E + e] *= 1.f + s[e];
+                }
+                if (HAS_H) {
+                    if (a.gate) load_vec<E>(q + u * E, a.gate + g * a.ld_gate + c);
+                    if (a.w_post) {
+                        load_vec<E>(s, a.w_post + c);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((u * T + t) * E < C) {
-#pragma unroll
-                    for (int i = u * E; i < u * E + E; ++i) {
-                        h[i] *= rh_;
-                        sB[i] = fmaf(d[i], h[i], sB[i]);
-                        d[i] *= gate[i];
-                        s[0] += d[i];
-                        s[1] = fmaf(d[i], h[i], s[1]);
+                        for (int e = 0; e < E; ++e) q[u * E + e] *= s[e];
                     }
                 }
-            float md = 0.f, mdn = 0.f;
-            if (a.post != PRISM_NORM_NONE) {
-                team.sum(s);
-                md = a.post == PRISM_NORM_LAYER ? s[0] * inv_c : 0.f;
-                mdn = s[1] * inv_c;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mul[i] = f2(in(2 * i) ? m[2 * i] : 0.f, in(2 * i + 1) ? m[2 * i + 1] : 0.f);
+            if constexpr (HAS_H) gate[i] = f2(in(2 * i) ? q[2 * i] : 0.f, in(2 * i + 1) ? q[2 * i + 1] : 0.f);
+        }
+    }
+
+    F2 sA[4], sD[4], sB[HAS_H ? 4 : 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sA[i] = sD[i] = f2(0.f);
+        if constexpr (HAS_H) sB[i] = f2(0.f);
+    }
+
+    int stage = 0;
+    for (int64_t r = r0; r < r1; r += step) {
+        F2 z[4], dy[4], d[4], h[HAS_H ? 4 : 1];
+        if constexpr (RING) {
+            cp_wait<D - 1>();
+            const char* s = g_ring + stage * stage_bytes;
+            LX::read(z, s, threads, tid);
+            LH::read(dy, s + o_dy, threads, tid);
+            LX::read(d, s + o_dz, threads, tid);
+            if constexpr (HAS_H) LH::read(h, s + o_h, threads, tid);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[2];
+                unpack<1>(rz[2 * i], f); unpack<1>(rz[2 * i + 1], f + 1);
+                z[i] = f2(f[0], f[1]);
+                unpack<1>(rdy[2 * i], f); unpack<1>(rdy[2 * i + 1], f + 1);
+                dy[i] = f2(f[0], f[1]);
+                unpack<1>(rdz[2 * i], f); unpack<1>(rdz[2 * i + 1], f + 1);
+                d[i] = f2(f[0], f[1]);
+                if constexpr (HAS_H) {
+                    unpack<1>(rh[2 * i], f); unpack<1>(rh[2 * i + 1], f + 1);
+                    h[i] = f2(f[0], f[1]);
+                }
+            }
+            fetch(r + step, 0);
+        }
+
+        // means first (layer): of z, of c = dy ∘ mul and of h
+        constexpr int NS = BR == kNormed ? 3 : 2;
+        float mc = 0.f;
+        if (a.norm == PRISM_NORM_LAYER || (BR == kNormed && a.post == PRISM_NORM_LAYER)) {
+            F2 q[3] = {z[0], dy[0] * mul[0], HAS_H ? h[0] : z[0]};
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+                q[0] = q[0] + z[i];
+                q[1] = fma(dy[i], mul[i], q[1]);
+                if constexpr (BR == kNormed) q[2] = q[2] + h[i];
+            }
+            float s[NS];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) s[i] = sum(q[i]);
+            team.sum(s);
+            if (a.norm == PRISM_NORM_LAYER) {
+                const float mz = -mean_of(s[0], fc, inv_c);
+                mc = s[1] * inv_c;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = z[i] + pair(mz, i);
+            }
+            if constexpr (BR == kNormed) {
+                if (a.post == PRISM_NORM_LAYER) {
+                    const float mh = -mean_of(s[NS - 1], fc, inv_c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[i] = h[i] + pair(mh, i);
+                }
+            }
+        }
+        // second moments, and c against z
+        float rh_ = 1.f;
+        if (has_y || BR == kNormed) {
+            F2 q[3] = {z[0] * z[0], dy[0] * mul[0] * z[0], HAS_H ? h[0] * h[0] : z[0]};
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+                q[0] = fma(z[i], z[i], q[0]);
+                q[1] = fma(dy[i] * mul[i], z[i], q[1]);
+                if constexpr (BR == kNormed) q[2] = fma(h[i], h[i], q[2]);
+            }
+            float s[NS];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) s[i] = sum(q[i]);
+            team.sum(s);
+            if (has_y) {
+                const float rs = rsqrtf(s[0] * inv_c + a.eps), mcn = s[1] * rs * inv_c;
+                const F2 rs2 = f2(rs), mcn2 = f2(-mcn);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const F2 n = z[i] * rs2;
+                    sA[i] = fma(dy[i], n, sA[i]);
+                    sD[i] = sD[i] + dy[i];
+                    d[i] = fma(rs2, fma(n, mcn2, fma(dy[i], mul[i], pair(-mc, i))), d[i]);
+                }
+            }
+            if constexpr (BR == kNormed) rh_ = rsqrtf(s[NS - 1] * inv_c + a.eps);
+        }
+        auto put = [&](auto* row, const F2 (&v)[4]) {
+            using TO = typename std::remove_reference<decltype(*row)>::type;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = both(v[i]);
+                o[2 * i] = f.x;
+                o[2 * i + 1] = f.y;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int c = (u * T + t) * E;
                 if (c < C) {
-                    float o[E];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] = rh_ * (d[u * E + e] - md - h[u * E + e] * mdn);
-                    Pack<TH, E> p;
-                    pack<E>(p, o);
-                    store((TH*)a.dh + r * a.ld_dh + c, p);
+                    Pack<TO, E> p;
+                    pack<E>(p, o + u * E);
+                    store(row + c, p);
                 }
             }
+        };
+        {
+            F2 o[4];
+            const F2 res = f2(HAS_H ? a.res : 1.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = HAS_H ? d[i] * res : d[i];
+            put((TX*)a.dx + r * a.ld_dx, o);
+        }
+        if constexpr (HAS_H) {
+            F2 q[2] = {f2(0.f), f2(0.f)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (BR == kNormed) h[i] = h[i] * f2(rh_);
+                sB[i] = fma(d[i], h[i], sB[i]);
+                d[i] = d[i] * gate[i];
+                if constexpr (BR == kNormed) {
+                    q[0] = q[0] + d[i];
+                    q[1] = fma(d[i], h[i], q[1]);
+                }
+            }
+            if constexpr (BR == kNormed) {
+                float s[2] = {sum(q[0]), sum(q[1])};
+                team.sum(s);
+                const F2 md = f2(a.post == PRISM_NORM_LAYER ? -s[0] * inv_c : 0.f), mdn = f2(-s[1] * inv_c), rr = f2(rh_);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = rr * fma(h[i], mdn, d[i] + md);
+            }
+            put((TH*)a.dh + r * a.ld_dh, d);
+        }
+        if constexpr (RING) {             // the row's own values have been used: their place is free
+            fetch(r + D * step, stage);
+            stage = stage + 1 == D ? 0 : stage + 1;
         }
     }
+    if constexpr (RING) cp_wait<0>();
 
+    float fA[8], fD[8], fB[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 f = both(sA[i]);
+        fA[2 * i] = f.x; fA[2 * i + 1] = f.y;
+        f = both(sD[i]);
+        fD[2 * i] = f.x; fD[2 * i + 1] = f.y;
+        f = both(sB[HAS_H ? i : 0]);
+        fB[2 * i] = f.x; fB[2 * i + 1] = f.y;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int c = (u * T + t) * E;
         if (c >= C) continue;
         if (a.part) {
             float* p = a.part + seg * 3 * C + c;
-            store_vec<E>(p, sA + u * E);
-            store_vec<E>(p + C, sD + u * E);
-            if constexpr (HAS_H) store_vec<E>(p + 2 * C, sB + u * E);
+            store_vec<E>(p, fA + u * E);
+            store_vec<E>(p + C, fD + u * E);
+            if constexpr (HAS_H) store_vec<E>(p + 2 * C, fB + u * E);
         }
         if (a.dscale) {
             float w[E], b[E];
@@ -447,10 +517,10 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
             if (a.w) load_vec<E>(w, a.w + c);
             if (a.b) load_vec<E>(b, a.b + c);
 #pragma unroll
-            for (int e = 0; e < E; ++e) w[e] = fmaf(w[e], sA[u * E + e], b[e] * sD[u * E + e]);
+            for (int e = 0; e < E; ++e) w[e] = fmaf(w[e], fA[u * E + e], b[e] * fD[u * E + e]);
             store_vec<E>(a.dscale + g * C + c, w);
         }
-        if (a.dshift) store_vec<E>(a.dshift + g * C + c, sD + u * E);
+        if (a.dshift) store_vec<E>(a.dshift + g * C + c, fD + u * E);
         if constexpr (HAS_H) {
             if (a.dgate) {
                 float w[E];
@@ -458,7 +528,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
                 for (int e = 0; e < E; ++e) w[e] = 1.f;
                 if (a.w_post) load_vec<E>(w, a.w_post + c);
 #pragma unroll
-                for (int e = 0; e < E; ++e) w[e] *= sB[u * E + e];
+                for (int e = 0; e < E; ++e) w[e] *= fB[u * E + e];
                 store_vec<E>(a.dgate + g * C + c, w);
             }
         }
@@ -477,7 +547,7 @@ inline int cta_teams(int C) {
 }
 // the kernel's MAXT for a team, and the CTAs of at most that many threads that its registers leave room for on an SM
 constexpr int team_bucket(int threads) {
-    return threads <= 32 ? 32 : threads <= 256 ? 256 : threads <= 384 ? 384 : threads <= 512 ? 512 : threads <= 768 ? 768 : 1024;
+    return threads <= 32 ? 32 : threads <= 256 ? 256 : threads <= 384 ? 384 : threads <= 512 ? 512 : threads <= 640 ? 640 : threads <= 768 ? 768 : 1024;
 }
 constexpr int fwd_ctas(int maxt) { return maxt <= 256 ? 3 : maxt <= 384 ? 2 : 1; }
 constexpr int bwd_ctas(int maxt) { return maxt <= 256 ? 2 : 1; }
@@ -487,43 +557,64 @@ inline int sm_teams(int C, int ctas) {
     return ctas * most / t;
 }
 
+// rows ahead in the backward (2: 5% slower, 4: the same), fewer where the widest rows leave no room
+constexpr int kRowsAhead = 3;
+template <typename TX, typename TH, int E, int MAXT, int H>
+prism_status_t launch_bwd_one(const BwdArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
+    constexpr int CTAS = bwd_ctas(MAXT), row = 8 * (int)(2 * sizeof(TX) + (H ? 2 : 1) * sizeof(TH));
+    constexpr int threads = MAXT == 32 ? 256 : MAXT;
+    constexpr int most = (200 << 10) / (row * threads * CTAS), D = most < 1 ? 1 : most > kRowsAhead ? kRowsAhead : most;
+    auto kernel = &k_block_norm_bwd<TX, TH, E, MAXT, H, CTAS, D>;
+    const int bytes = Lane<TX, E>::kAsync && Lane<TH, E>::kAsync ? D * row * (int)(block.x * block.y) : 0;
+    // with the static part, more than the 48 KB that need no leave
+    if (bytes > 40 << 10 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return PRISM_ERR_CUDA;
+    kernel<<<grid, block, bytes, s>>>(a);
+    return PRISM_OK;
+}
+template <typename TX, typename TH, int E, int MAXT, int H>
+prism_status_t launch_fwd_one(const FwdArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
+    k_block_norm_fwd<TX, TH, E, MAXT, H != kNoBranch, fwd_ctas(MAXT)><<<grid, block, 0, s>>>(a);
+    return PRISM_OK;
+}
+
 // one launcher a pair of types (stream, branch); unit = channels an access
-template <typename TX, typename TH> void launch_fwd(const FwdArgs& a, int unit, cudaStream_t s);
-template <typename TX, typename TH> void launch_bwd(const BwdArgs& a, int unit, cudaStream_t s);
+template <typename TX, typename TH> prism_status_t launch_fwd(const FwdArgs& a, int unit, cudaStream_t s);
+template <typename TX, typename TH> prism_status_t launch_bwd(const BwdArgs& a, int unit, cudaStream_t s);
 
-#define PRISM_BN_BY_SIZE(KERNEL, CTAS, TX, TH, E, H)                                                     \
-    do {                                                                                                \
-        switch (team_bucket(block.x)) {                                                                 \
-            case 32: KERNEL<TX, TH, E, 32, H, CTAS(32)><<<grid, block, 0, s>>>(a); break;               \
-            case 256: KERNEL<TX, TH, E, 256, H, CTAS(256)><<<grid, block, 0, s>>>(a); break;            \
-            case 384: KERNEL<TX, TH, E, 384, H, CTAS(384)><<<grid, block, 0, s>>>(a); break;            \
-            case 512: KERNEL<TX, TH, E, 512, H, CTAS(512)><<<grid, block, 0, s>>>(a); break;            \
-            case 768: KERNEL<TX, TH, E, 768, H, CTAS(768)><<<grid, block, 0, s>>>(a); break;            \
-            default: KERNEL<TX, TH, E, 1024, H, CTAS(1024)><<<grid, block, 0, s>>>(a); break;           \
-        }                                                                                               \
-    } while (0)
+#define PRISM_BN_BY_SIZE(ONE, TX, TH, E, H)                                            \
+    switch (team_bucket(block.x)) {                                                   \
+        case 32: return ONE<TX, TH, E, 32, H>(a, grid, block, s);                     \
+        case 256: return ONE<TX, TH, E, 256, H>(a, grid, block, s);                   \
+        case 384: return ONE<TX, TH, E, 384, H>(a, grid, block, s);                   \
+        case 512: return ONE<TX, TH, E, 512, H>(a, grid, block, s);                   \
+        case 640: return ONE<TX, TH, E, 640, H>(a, grid, block, s);                   \
+        case 768: return ONE<TX, TH, E, 768, H>(a, grid, block, s);                   \
+        default: return ONE<TX, TH, E, 1024, H>(a, grid, block, s);                   \
+    }
 
-#define PRISM_BN_BY_UNIT(KERNEL, CTAS, TX, TH, H)                                      \
+#define PRISM_BN_BY_UNIT(ONE, TX, TH, H)                                              \
     do {                                                                              \
-        if (unit == 8) PRISM_BN_BY_SIZE(KERNEL, CTAS, TX, TH, 8, H);                  \
-        else if (unit == 2) PRISM_BN_BY_SIZE(KERNEL, CTAS, TX, TH, 2, H);             \
-        else PRISM_BN_BY_SIZE(KERNEL, CTAS, TX, TH, 1, H);                            \
+        if (unit == 8) PRISM_BN_BY_SIZE(ONE, TX, TH, 8, H)                            \
+        if (unit == 2) PRISM_BN_BY_SIZE(ONE, TX, TH, 2, H)                            \
+        PRISM_BN_BY_SIZE(ONE, TX, TH, 1, H)                                           \
     } while (0)
 
 #define PRISM_BN_INSTANTIATE(TX, TH)                                                                   \
-    template <> void launch_fwd<TX, TH>(const FwdArgs& a, int unit, cudaStream_t s) {                  \
+    template <> prism_status_t launch_fwd<TX, TH>(const FwdArgs& a, int unit, cudaStream_t s) {        \
         const dim3 block(team_threads(a.C), cta_teams(a.C));                                           \
         const int64_t want = (a.R + block.y - 1) / block.y;                                            \
         const int64_t most = kSMs * (int64_t)sm_teams(a.C, fwd_ctas(team_bucket(block.x))) / block.y;  \
         const dim3 grid((unsigned)(want < most ? want : most));                                        \
-        if (a.h) PRISM_BN_BY_UNIT(k_block_norm_fwd, fwd_ctas, TX, TH, true);                           \
-        else PRISM_BN_BY_UNIT(k_block_norm_fwd, fwd_ctas, TX, TH, false);                              \
+        if (a.h) PRISM_BN_BY_UNIT(launch_fwd_one, TX, TH, kPlain);                                     \
+        else PRISM_BN_BY_UNIT(launch_fwd_one, TX, TH, kNoBranch);                                      \
     }                                                                                                  \
-    template <> void launch_bwd<TX, TH>(const BwdArgs& a, int unit, cudaStream_t s) {                  \
+    template <> prism_status_t launch_bwd<TX, TH>(const BwdArgs& a, int unit, cudaStream_t s) {        \
         const dim3 block(team_threads(a.C), cta_teams(a.C));                                           \
         const dim3 grid((unsigned)((a.segs + block.y - 1) / block.y));                                 \
-        if (a.h) PRISM_BN_BY_UNIT(k_block_norm_bwd, bwd_ctas, TX, TH, true);                           \
-        else PRISM_BN_BY_UNIT(k_block_norm_bwd, bwd_ctas, TX, TH, false);                              \
+        if (a.h && a.post != PRISM_NORM_NONE) PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kNormed);       \
+        else if (a.h) PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kPlain);                                \
+        else PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kNoBranch);                                      \
     }
 
 }  // namespace bn

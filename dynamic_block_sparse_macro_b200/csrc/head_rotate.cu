@@ -7,8 +7,8 @@
 // and backwards, with dn the pairs of dr turned back (by -angle), c = dn ∘ w, n = x r:
 //   dx = r (c - n mean(c ∘ n)),  dw = sum over tokens and heads of dn ∘ n.
 //
-// Bound by HBM: each element is read and written once.  d/8 lanes hold a head's row, eight channels
-// each, and walk the heads of one token, so that the token's place, its cosines and its sines (a
+// Bound by HBM: each element is read and written once.  d/8 lanes hold a head's row, four channel pairs
+// each, so that a pair turns within its lane in either pairing, and walk the heads of one token, so that the token's place, its cosines and its sines (a
 // table of one row an axis position, which stays in L1) are fetched once for all its heads.  All
 // arithmetic is fp32; the result is rounded once.
 #include <initializer_list>
@@ -37,133 +37,212 @@ struct Args {
     float eps;
 };
 
+// Sums over the LPH lanes of a head.  Of two values each half of the lanes takes one over, so that the second
+// costs one exchange more and not as many again.
 template <int LPH> __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-
-// cosine and sine of the lane's pairs for one token
-template <int D, bool HALF>
-__device__ __forceinline__ void angles(const Args& a, int64_t token, int l, float* cs, float* sn) {
-    const uint32_t hw = (uint32_t)a.H * a.W;
-    const uint32_t at = (uint32_t)(token % ((int64_t)a.T * hw));
-    const uint32_t pt = at / hw, r = at - pt * hw, ph = r / a.W, pw = r - ph * a.W;
-    constexpr int NP = HALF ? 8 : 4;
-    const int p0 = HALF ? (l % (D / 16)) * 8 : l * 4;
+template <int LPH> __device__ __forceinline__ void lanes_sum(float& v, float& w, int l) {
+    const bool hi = l & (LPH / 2);
+    float k = (hi ? w : v) + __shfl_xor_sync(0xffffffffu, hi ? v : w, LPH / 2);
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        const int p = p0 + j, q = p - a.nT, s = q - a.nH;
-        float2 v = make_float2(1.f, 0.f);
-        if (p < a.nT) v = __ldg(a.table + pt * a.nT + p);
-        else if (q < a.nH) v = __ldg(a.table + a.T * a.nT + ph * a.nH + q);
-        else if (s < a.nW) v = __ldg(a.table + a.T * a.nT + a.H * a.nH + pw * a.nW + s);
-        cs[j] = v.x;
-        sn[j] = v.y;
-    }
+    for (int o = LPH / 4; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+    const float other = __shfl_xor_sync(0xffffffffu, k, LPH / 2);
+    v = hi ? other : k;
+    w = hi ? k : other;
 }
 
-// turns the lane's eight channels by the angle (dir = 1) or back (dir = -1)
-template <int D, bool HALF>
-__device__ __forceinline__ void turn(float (&v)[8], const float* cs, const float* sn, int l, float dir) {
+// A lane's four channel pairs: the first members in a, the second in b.
+struct Pairs {
+    F2 a[2], b[2];
+};
+// as they lie in memory: eight channels in a row (interleaved), or four of each half of the head
+template <typename T, bool HALF> struct Raw {
+    Pack<T, HALF ? 4 : 8> p[HALF ? 2 : 1];
+};
+template <int D, bool HALF> __device__ __forceinline__ int lane_at(int l) { return HALF ? 4 * l : 8 * l; }
+template <typename T, int D, bool HALF> __device__ __forceinline__ void load_raw(Raw<T, HALF>& r, const T* head) {
+    load(r.p[0], head);
+    if constexpr (HALF) load(r.p[1], head + D / 2);
+}
+template <typename T, bool HALF> __device__ __forceinline__ Pairs pairs_of(const Raw<T, HALF>& r) {
+    Pairs v;
     if constexpr (HALF) {
-        // the pair's other half lies d/16 lanes away: the first half gets a cos - b sin, the second b cos + a sin
-        const float s = l < D / 16 ? -dir : dir;
+        float a[4], b[4];
+        unpack<4>(r.p[0], a);
+        unpack<4>(r.p[1], b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float o = __shfl_xor_sync(0xffffffffu, v[j], D / 16);
-            v[j] = fmaf(v[j], cs[j], s * sn[j] * o);
+        for (int i = 0; i < 2; ++i) {
+            v.a[i] = f2(a[2 * i], a[2 * i + 1]);
+            v.b[i] = f2(b[2 * i], b[2 * i + 1]);
         }
     } else {
+        float f[8];
+        unpack<8>(r.p[0], f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float p = v[2 * j], q = v[2 * j + 1], s = dir * sn[j];
-            v[2 * j] = fmaf(p, cs[j], -s * q);
-            v[2 * j + 1] = fmaf(p, s, q * cs[j]);
+        for (int i = 0; i < 2; ++i) {
+            v.a[i] = f2(f[4 * i], f[4 * i + 2]);
+            v.b[i] = f2(f[4 * i + 1], f[4 * i + 3]);
         }
+    }
+    return v;
+}
+template <typename T, int D, bool HALF> __device__ __forceinline__ void store_pairs(T* head, const Pairs& v) {
+    float a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float2 f = both(v.a[i]);
+        a[2 * i] = f.x; a[2 * i + 1] = f.y;
+        f = both(v.b[i]);
+        b[2 * i] = f.x; b[2 * i + 1] = f.y;
+    }
+    if constexpr (HALF) {
+        Pack<T, 4> p;
+        pack<4>(p, a);
+        store(head, p);
+        pack<4>(p, b);
+        store(head + D / 2, p);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { f[2 * i] = a[i]; f[2 * i + 1] = b[i]; }
+        Pack<T, 8> p;
+        pack<8>(p, f);
+        store(head, p);
+    }
+}
+// per-channel floats of a lane (weights, their sums)
+template <int D, bool HALF> __device__ __forceinline__ int channel(int l, int i, bool second) {
+    return HALF ? 4 * l + i + (second ? D / 2 : 0) : 8 * l + 2 * i + second;
+}
+
+// cosine and sine of the lane's pairs for one token
+__device__ __forceinline__ void angles(const Args& a, uint32_t token, int l, F2 (&cs)[2], F2 (&sn)[2]) {
+    const uint32_t hw = (uint32_t)a.H * a.W, at = token % ((uint32_t)a.T * hw);
+    const uint32_t pt = at / hw, r = at - pt * hw, ph = r / a.W, pw = r - ph * a.W;
+    float2 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int p = l * 4 + j, q = p - a.nT, s = q - a.nH;
+        const int at_t = pt * a.nT + p, at_h = a.T * a.nT + ph * a.nH + q, at_w = a.T * a.nT + a.H * a.nH + pw * a.nW + s;
+        v[j] = make_float2(1.f, 0.f);
+        if (s < a.nW) v[j] = __ldg(a.table + (q < 0 ? at_t : s < 0 ? at_h : at_w));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        cs[i] = f2(v[2 * i].x, v[2 * i + 1].x);
+        sn[i] = f2(v[2 * i].y, v[2 * i + 1].y);
     }
 }
 
+// CTAs on an SM and heads of a lane on their way at a time: what the registers allow without spills, at 24 heads of 128
+// channels.  Forward: bf16 5 x 2 1150 us, 3 x 4 1182, 4 x 4 1206 (294912 tokens); f32 3 x 4 251-271, 5 x 2 266-295
+// (30720).  Backward: bf16 3 x 2 401 us, 2 x 2 485, 4 x 1 466 (61440 tokens); f32 2 x 2 355, 3 x 2 437 (30720).
+constexpr int ctas_sm(int elem, bool bwd) { return bwd ? (elem == 2 ? 3 : 2) : elem == 2 ? 5 : 3; }
+constexpr int heads_at_once(int elem, bool bwd) { return bwd || elem == 2 ? 2 : 4; }
+
 template <typename T, int D, bool HALF, bool BWD>
-__global__ void __launch_bounds__(256) k_head_rotate(const Args a) {
+__global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(const Args a) {
     constexpr int LPH = D / 8, TPW = 32 / LPH;       // lanes a head, heads a warp
-    constexpr int HU = BWD ? 2 : 4;                  // heads of a lane in flight
+    constexpr int HU = heads_at_once(sizeof(T), BWD);
     const Side& sd = a.side[blockIdx.y];
     const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH;
+    // the same for all lanes, and so known to the compiler: its step's counters and rows need no registers of theirs
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
     const int64_t warps = (int64_t)gridDim.x * 8, items = a.tokens * sd.parts;
-    const int stride = TPW * sd.parts;
-    float w[8], dw[8];
+    const int stride = TPW * sd.parts, c0 = lane_at<D, HALF>(l);
+    const F2 zero = f2(0.f);
+    Pairs w, dw;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) { w[j] = 1.f; dw[j] = 0.f; }
-    if (sd.w) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __ldg(sd.w + l * 8 + j);
+    for (int i = 0; i < 2; ++i) {
+        w.a[i] = w.b[i] = f2(1.f);
+        dw.a[i] = dw.b[i] = zero;
+        if (sd.w) {
+            w.a[i] = f2(__ldg(sd.w + channel<D, HALF>(l, 2 * i, false)), __ldg(sd.w + channel<D, HALF>(l, 2 * i + 1, false)));
+            w.b[i] = f2(__ldg(sd.w + channel<D, HALF>(l, 2 * i, true)), __ldg(sd.w + channel<D, HALF>(l, 2 * i + 1, true)));
+        }
     }
-    for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += warps) {
-        const int64_t token = it / sd.parts;
-        const int first = (int)(it - token * sd.parts) * TPW + sub;
-        const T* x = (const T*)sd.x + token * sd.ld_x + l * 8;
-        const T* dr = BWD ? (const T*)sd.dr + token * sd.ld_dr + l * 8 : nullptr;
-        T* out = (T*)sd.out + token * sd.ld_out + l * 8;
-        float cs[8], sn[8];
-        angles<D, HALF>(a, token, l, cs, sn);
-        // every lane of the warp takes part in the shuffles of every step: first - sub is the warp's
-        for (int h0 = first - sub; h0 < sd.heads; h0 += HU * stride) {
-            Pack<T, 8> px[HU], pr[BWD ? HU : 1];
+    for (int64_t it = (int64_t)blockIdx.x * 8 + warp; it < items; it += warps) {
+        const uint32_t token = sd.parts == 1 ? (uint32_t)it : (uint32_t)(it / sd.parts);
+        const int first = (int)(it - (int64_t)token * sd.parts) * TPW;
+        const T* x = (const T*)sd.x + (int64_t)token * sd.ld_x + c0;
+        const T* dr = BWD ? (const T*)sd.dr + (int64_t)token * sd.ld_dr + c0 : nullptr;
+        T* out = (T*)sd.out + (int64_t)token * sd.ld_out + c0;
+        F2 cs[2], sn[2], sm[2];                      // sm = -sn
+        // Every lane of the warp takes part in the exchanges of every step.  Lanes past the last head repeat it; they
+        // neither store nor add to dw.
+        for (int h0 = first; h0 < sd.heads; h0 += HU * stride) {
+            Raw<T, HALF> px[HU], pr[BWD ? HU : 1];
+            bool in[HU];
 #pragma unroll
             for (int u = 0; u < HU; ++u) {
-                const int h = h0 + sub + u * stride;
-                if (h < sd.heads) {
-                    if (!BWD || a.norm) load(px[u], x + h * D);
-                    if constexpr (BWD) load(pr[u], dr + h * D);
-                }
+                int h = h0 + sub + u * stride;
+                in[u] = h < sd.heads;
+                h = in[u] ? h : sd.heads - 1;
+                if (!BWD || a.norm) load_raw<T, D, HALF>(px[u], x + h * D);
+                if constexpr (BWD) load_raw<T, D, HALF>(pr[u], dr + h * D);
+            }
+            if (h0 == first) {
+                angles(a, token, l, cs, sn);
+                sm[0] = sn[0] * f2(-1.f);
+                sm[1] = sn[1] * f2(-1.f);
             }
 #pragma unroll
             for (int u = 0; u < HU; ++u) {
-                const int h = h0 + sub + u * stride;
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.f;
-                if (h < sd.heads && (!BWD || a.norm)) unpack<8>(px[u], v);
-                float r = 1.f;
-                if (a.norm) {
-                    float q = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) q = fmaf(v[j], v[j], q);
-                    r = rsqrtf(lanes_sum<LPH>(q) * (1.f / D) + a.eps);
-                }
+                Pairs v, o;
+                if (!BWD || a.norm) v = pairs_of<T, HALF>(px[u]);
                 if constexpr (!BWD) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] *= r * w[j];
-                    turn<D, HALF>(v, cs, sn, l, 1.f);
-                } else {
-                    float d[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) d[j] = 0.f;
-                    if (h < sd.heads) unpack<8>(pr[u], d);
-                    turn<D, HALF>(d, cs, sn, l, -1.f);
                     if (a.norm) {
-                        float m = 0.f;
+                        const float q = lanes_sum<LPH>(sum(fma(v.a[0], v.a[0], v.a[1] * v.a[1]) +
+                                                           fma(v.b[0], v.b[0], v.b[1] * v.b[1])));
+                        const F2 r = f2(rsqrtf(q * (1.f / D) + a.eps));
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            v[j] *= r;
-                            dw[j] = fmaf(d[j], v[j], dw[j]);
-                            d[j] *= w[j];
-                            m = fmaf(d[j], v[j], m);
+                        for (int i = 0; i < 2; ++i) {
+                            v.a[i] = v.a[i] * (r * w.a[i]);
+                            v.b[i] = v.b[i] * (r * w.b[i]);
                         }
-                        m = lanes_sum<LPH>(m) * (1.f / D);
+                    }
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = r * fmaf(-v[j], m, d[j]);
-                    } else {
+                    for (int i = 0; i < 2; ++i) {
+                        o.a[i] = fma(v.a[i], cs[i], v.b[i] * sm[i]);
+                        o.b[i] = fma(v.a[i], sn[i], v.b[i] * cs[i]);
+                    }
+                } else {
+                    const Pairs d = pairs_of<T, HALF>(pr[u]);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = d[j];
+                    for (int i = 0; i < 2; ++i) {
+                        o.a[i] = fma(d.a[i], cs[i], d.b[i] * sn[i]);
+                        o.b[i] = fma(d.b[i], cs[i], d.a[i] * sm[i]);
+                    }
+                    if (a.norm) {
+                        // x once against itself, once against dn ∘ w; dx = r dn ∘ w - x r³ mean(dn ∘ w ∘ x)
+                        Pairs t;
+                        F2 q2 = v.a[0] * v.a[0], m2;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            t.a[i] = o.a[i] * v.a[i];
+                            t.b[i] = o.b[i] * v.b[i];
+                            if (i) q2 = fma(v.a[i], v.a[i], q2);
+                            q2 = fma(v.b[i], v.b[i], q2);
+                            m2 = i ? fma(t.a[i], w.a[i], m2) : t.a[i] * w.a[i];
+                            m2 = fma(t.b[i], w.b[i], m2);
+                        }
+                        float q = sum(q2), m = sum(m2);
+                        lanes_sum<LPH>(q, m, l);
+                        const float r = rsqrtf(q * (1.f / D) + a.eps);
+                        const F2 r2 = f2(r), rd = f2(in[u] ? r : 0.f), k = f2(-(r * r) * (r * m) * (1.f / D));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            dw.a[i] = fma(t.a[i], rd, dw.a[i]);
+                            dw.b[i] = fma(t.b[i], rd, dw.b[i]);
+                            o.a[i] = fma(v.a[i], k, o.a[i] * w.a[i] * r2);
+                            o.b[i] = fma(v.b[i], k, o.b[i] * w.b[i] * r2);
+                        }
                     }
                 }
-                if (h < sd.heads) {
-                    Pack<T, 8> o;
-                    pack<8>(o, v);
-                    store(out + h * D, o);
-                }
+                if (in[u]) store_pairs<T, D, HALF>(out + (h0 + sub + u * stride) * D, o);
             }
         }
     }
@@ -172,7 +251,14 @@ __global__ void __launch_bounds__(256) k_head_rotate(const Args a) {
         __shared__ float sh[256 / LPH][D];
         const int team = threadIdx.x / LPH;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sh[team][l * 8 + j] = dw[j];
+        for (int i = 0; i < 2; ++i) {
+            float2 f = both(dw.a[i]);
+            sh[team][channel<D, HALF>(l, 2 * i, false)] = f.x;
+            sh[team][channel<D, HALF>(l, 2 * i + 1, false)] = f.y;
+            f = both(dw.b[i]);
+            sh[team][channel<D, HALF>(l, 2 * i, true)] = f.x;
+            sh[team][channel<D, HALF>(l, 2 * i + 1, true)] = f.y;
+        }
         __syncthreads();
         if (threadIdx.x < D) {
             float s = 0.f;
@@ -198,12 +284,12 @@ __global__ void __launch_bounds__(512) k_head_rotate_join(const float* part, int
     }
 }
 
-constexpr int kMaxCtas = kSMs * 6;
+constexpr int kMaxCtas = kSMs * 5;     // as many as run at a time
 
 static prism_status_t check(const prism_rotate_t* p) {
     if (!p) return PRISM_ERR_INVALID_ARG;
     if (p->tokens < 0 || p->T < 1 || p->H < 1 || p->W < 1) return PRISM_ERR_SHAPE;
-    if (p->tokens > (int64_t(1) << 40) || (int64_t)p->T * p->H * p->W > INT32_MAX ||
+    if (p->tokens > INT32_MAX || (int64_t)p->T * p->H * p->W > INT32_MAX ||
         (int64_t)p->T * p->pairs_t + (int64_t)p->H * p->pairs_h + (int64_t)p->W * p->pairs_w > INT32_MAX)
         return PRISM_ERR_UNSUPPORTED;
     if (p->dtype != PRISM_F32 && p->dtype != PRISM_BF16) return PRISM_ERR_UNSUPPORTED;
@@ -232,13 +318,13 @@ static int parts_of(int64_t tokens, int heads, int d) {
     return want < 1 ? 1 : (int)want;
 }
 
-static unsigned ctas_of(const Args& a, int sides) {
+static unsigned ctas_of(const Args& a, int sides, int per_sm) {
     int64_t items = 0;
     for (int i = 0; i < sides; ++i) {
         const int64_t n = a.tokens * a.side[i].parts;
         if (n > items) items = n;
     }
-    const int64_t want = (items + 7) / 8, most = kMaxCtas / sides;
+    const int64_t want = (items + 7) / 8, most = (int64_t)kSMs * per_sm / sides;
     return (unsigned)(want < most ? want : most);
 }
 
@@ -305,7 +391,7 @@ static prism_status_t rotate(const prism_rotate_t* p, const void* Q, const void*
     a.T = p->T; a.H = p->H; a.W = p->W;
     a.nT = p->pairs_t; a.nH = p->pairs_h; a.nW = p->pairs_w;
     a.norm = p->norm; a.eps = p->eps;
-    const unsigned ctas = ctas_of(a, sides);
+    const unsigned ctas = ctas_of(a, sides, ctas_sm(p->dtype == PRISM_BF16 ? 2 : 4, bwd));
     const dim3 grid(ctas, sides);
     if (!bwd) {
         launch<false>(p, a, grid, stream);

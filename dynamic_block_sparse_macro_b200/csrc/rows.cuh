@@ -90,6 +90,112 @@ template <int N> __device__ __forceinline__ void pack(Pack<__nv_bfloat16, N>& p,
     }
 }
 
+// Two fp32 values in one 64-bit register: sm_100a adds, multiplies and fuses both with one instruction.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float2 both(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float sum(F2 a) {
+    const float2 f = both(a);
+    return f.x + f.y;
+}
+__device__ __forceinline__ void unpack2(const Pack<float, 8>& p, F2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(p.w[2 * i]), __uint_as_float(p.w[2 * i + 1]));
+}
+__device__ __forceinline__ void unpack2(const Pack<__nv_bfloat16, 8>& p, F2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(p.w[i] << 16), __uint_as_float(p.w[i] & 0xffff0000u));
+}
+
+// A row's elements on their way from HBM: each thread copies what it will itself read into its own part of
+// shared memory, rows ahead of their use, without registers and without a barrier (it waits for its own copies).
+// Memory is laid out in planes of one access a thread, so that a warp's accesses are contiguous.
+template <int B> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    static_assert(B == 4 || B == 8 || B == 16, "an access of cp.async");
+    if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else if constexpr (B == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T, int E> struct Lane {
+    static constexpr int U = 8 / E;                                     // units of E channels: eight channels a thread
+    static constexpr bool kAsync = sizeof(T) * E >= 4;
+    static constexpr int B = sizeof(T) * E < 16 ? (int)sizeof(T) * E : 16, P = (int)sizeof(T) * E / B;
+    static constexpr int kBytes = 8 * (int)sizeof(T);                   // of a thread and row
+    // unit u of thread t in a team of `team` threads covers channels (u * team + t) * E + [0, E)
+    static __device__ __forceinline__ void fetch(uint32_t s, int threads, int tid, const T* row, int t, int team, int C) {
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (u * team + t) * E;
+                if (c < C) {
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        cp_async<B>(s + (uint32_t)(((u * P + p) * threads + tid) * B), row + c + p * (B / (int)sizeof(T)));
+                }
+            }
+        }
+    }
+    // places that no copy writes (past the row's end, or `all`) hold 0
+    static __device__ __forceinline__ void clear(char* s, int threads, int tid, int t, int team, int C, bool all) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (all || (u * team + t) * E >= C) {
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int i = 0; i < B; i += 4)
+                        *reinterpret_cast<uint32_t*>(s + ((u * P + p) * threads + tid) * B + i) = 0u;
+            }
+    }
+    // the thread's eight channels in fp32
+    static __device__ __forceinline__ void read(F2 (&f)[4], const char* s, int threads, int tid) {
+        Pack<T, 8> v;
+#pragma unroll
+        for (int i = 0; i < U * P; ++i) {
+            const char* a = s + (i * threads + tid) * B;
+            if constexpr (B == 16) {
+                const uint4 q = *reinterpret_cast<const uint4*>(a);
+                v.w[4 * i] = q.x; v.w[4 * i + 1] = q.y; v.w[4 * i + 2] = q.z; v.w[4 * i + 3] = q.w;
+            } else if constexpr (B == 8) {
+                const uint2 q = *reinterpret_cast<const uint2*>(a);
+                v.w[2 * i] = q.x; v.w[2 * i + 1] = q.y;
+            } else if constexpr (B == 4) {
+                v.w[i] = *reinterpret_cast<const uint32_t*>(a);
+            }
+        }
+        unpack2(v, f);
+    }
+};
+
 // s / c, where 1 / c is at hand: one correction makes it exact where the quotient is
 __device__ __forceinline__ float mean_of(float s, float c, float inv_c) {
     const float m = s * inv_c;
@@ -103,12 +209,13 @@ __device__ __forceinline__ float mean_of(float s, float c, float inv_c) {
 // named barrier, took 30% longer.)
 template <int MAXT> struct Team {
     static constexpr int W = MAXT <= 256 ? 8 : MAXT <= 512 ? 16 : 32;   // warps of a team at most
-    static constexpr int kBufs = MAXT == 32 ? 1 : 2 * W;
-    float4* buf;       // [2][W]
+    static constexpr int kFloats = MAXT == 32 ? 1 : 2 * 4 * W;
+    float* buf;        // [2][4][W]
     uint32_t mask;     // of the team's lanes in a warp
     int flip;
 
-    __device__ __forceinline__ void init(float4* smem) {
+    // by all threads of the CTA
+    __device__ __forceinline__ void init(float* smem) {
         buf = smem;
         flip = 0;
         mask = 0xffffffffu;
@@ -116,10 +223,16 @@ template <int MAXT> struct Team {
             const int lane = (threadIdx.y * blockDim.x + threadIdx.x) & 31;
             mask = ((1u << blockDim.x) - 1) << (lane & ~(blockDim.x - 1));
         }
+        if (MAXT > 32) {                                 // the places of warps that the CTA does not have count as 0
+            for (int i = threadIdx.x; i < kFloats; i += blockDim.x) smem[i] = 0.f;
+            __syncthreads();
+        }
     }
-    // sums of up to four values over the team, in a fixed order
+    // Sums of up to four values over the team, in a fixed order.  A warp's lanes share the values out among them:
+    // with four, the halves of the warp swap two each, the quarters one, and three steps finish each lane's value
+    // (6 exchanges instead of 20); the warps' sums meet in the same way.
     template <int N> __device__ __forceinline__ void sum(float (&v)[N]) {
-        static_assert(N <= 4, "four values");
+        static_assert(N >= 1 && N <= 4, "up to four values");
         if constexpr (MAXT == 32) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
@@ -128,24 +241,38 @@ template <int MAXT> struct Team {
                     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(mask, v[i], o);
                 }
         } else {
+            constexpr int NP = N <= 2 ? N : 4, L = 32 / NP;
+            const int l = threadIdx.x & 31;
+            float a[NP];
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-            float4* b = buf + flip * W;
+            for (int i = 0; i < NP; ++i) a[i] = i < N ? v[i] : 0.f;
+            int o = 16;
+#pragma unroll
+            for (int c = NP / 2; c > 0; c >>= 1, o >>= 1) {
+                const bool hi = l & o;
+#pragma unroll
+                for (int i = 0; i < c; ++i) {
+                    const float give = hi ? a[i] : a[i + c], keep = hi ? a[i + c] : a[i];
+                    a[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            }
+            float k = a[0];
+#pragma unroll
+            for (; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+            // lane l has value l / L
+            float* b = buf + flip * 4 * W;
             flip ^= 1;
-            const int l = threadIdx.x & 31, i = l & (W - 1);
-            if (l == 0)
-                b[threadIdx.x >> 5] = make_float4(v[0], N > 1 ? v[N > 1 ? 1 : 0] : 0.f, N > 2 ? v[N > 2 ? 2 : 0] : 0.f,
-                                                  N > 3 ? v[N > 3 ? 3 : 0] : 0.f);
+            if (l % L == 0) b[l / L * W + (threadIdx.x >> 5)] = k;
             __syncthreads();
-            const float4 q = i < (blockDim.x >> 5) ? b[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[0] = q.x;
-            if constexpr (N > 1) v[1] = q.y;
-            if constexpr (N > 2) v[2] = q.z;
-            if constexpr (N > 3) v[3] = q.w;
+            constexpr int PARTS = L < W ? L : W, PER = W / PARTS;       // lanes a value, warps a lane
+            const float* q = b + (l % NP) * W + (l / NP % PARTS) * PER;
+            k = q[0];
 #pragma unroll
-            for (int o = W / 2; o > 0; o >>= 1)
+            for (int i = 1; i < PER; ++i) k += q[i];
 #pragma unroll
-                for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+            for (int p = NP; p < NP * PARTS; p <<= 1) k += __shfl_xor_sync(0xffffffffu, k, p);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = NP == 1 ? k : __shfl_sync(0xffffffffu, k, i);
         }
     }
     __device__ __forceinline__ float sum1(float a) {

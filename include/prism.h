@@ -576,7 +576,7 @@ prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, const void* z, 
  */
 typedef enum { PRISM_PAIRS_INTERLEAVED = 0, PRISM_PAIRS_HALF = 1 } prism_pairing_t;
 typedef struct {
-    int64_t tokens;                       /* >= 0                                 */
+    int64_t tokens;                       /* 0 .. 2^31 - 1                        */
     int32_t T, H, W;                      /* >= 1, any                            */
     int32_t heads_q, heads_k, head_dim;   /* 0 .. 1024 each; 64 or 128            */
     int32_t pairs_t, pairs_h, pairs_w;    /* sum <= head_dim / 2                  */
