@@ -7,8 +7,6 @@
 namespace prism {
 namespace bn {
 
-constexpr int kMaxJoin = 64;
-
 template <> prism_status_t launch_fwd<float, float>(const FwdArgs&, int, cudaStream_t);
 template <> prism_status_t launch_fwd<float, __nv_bfloat16>(const FwdArgs&, int, cudaStream_t);
 template <> prism_status_t launch_fwd<__nv_bfloat16, __nv_bfloat16>(const FwdArgs&, int, cudaStream_t);
@@ -21,115 +19,159 @@ struct JoinArgs {
     const float *w, *b, *w_post, *scale, *gate;
     float *dgate, *dscale, *dshift;     // [groups][C]
     float *dw, *db, *dw_post;           // [C]
-    float* part2;                       // [gridDim.y][3][C] where gridDim.y > 1
     int64_t groups, segs, ld_scale, ld_gate;
-    int C, per_group;
+    int C, per_group, wide;             // per_group as in BwdArgs
 };
 
-// 32 channels a CTA, 16 rows of threads that take every 16th segment; their sums meet in a fixed
-// order, so the result does not depend on scheduling.
-__device__ __forceinline__ void join_rows(float (&v)[3], float (*sh)[3][32]) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) sh[threadIdx.y][i][threadIdx.x] = v[i];
-    __syncthreads();
-    if (threadIdx.y == 0) {
-#pragma unroll
-        for (int y = 1; y < 16; ++y)
-#pragma unroll
-            for (int i = 0; i < 3; ++i) v[i] += sh[y][i][threadIdx.x];
-    }
-    __syncthreads();
-}
-
-__global__ void __launch_bounds__(512) k_block_norm_groups(const JoinArgs a) {
-    __shared__ float sh[16][3][32];
-    const int c = blockIdx.x * 32 + threadIdx.x;
-    for (int64_t g = blockIdx.y; g < a.groups; g += gridDim.y) {
-        float v[3] = {0.f, 0.f, 0.f};
-        if (c < a.C) {
+// The segments' column sums to the vectors' gradients.  32 channels a CTA, whose 16 warps take every 16th segment.
+// The CTAs of a cluster share the work out among them: the segments of each group in turn where groups are few and
+// long (`wide`), the segments where each has whole groups, else the groups; the first of them adds up what the others
+// have.  All in a
+// fixed order, so that the result does not depend on scheduling.
+constexpr int kJoinRows = 16, kMaxCluster = 8;
+__global__ void __launch_bounds__(32 * kJoinRows) k_block_norm_join(const JoinArgs a) {
+    __shared__ float sh[kJoinRows][3][32];
+    __shared__ float sums[3][32];
+    const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * 32 + x;
+    const bool in = c < a.C, affine = a.dw || a.db || a.dw_post;
+    const int64_t n = gridDim.y, me = blockIdx.y;
+    // v: the sums over the segments s0, s0 + 1, ... s1 - 1, in the threads y = 0
+    auto read = [&](int64_t s0, int64_t s1, float (&v)[3]) {
+        v[0] = v[1] = v[2] = 0.f;
+        if (in) {
+            const bool a0 = a.dscale || a.dw, a1 = a.dscale || a.dshift || a.db, a2 = a.dgate || a.dw_post;
 #pragma unroll 4
-            for (int s = threadIdx.y; s < a.per_group; s += 16) {
-                const float* p = a.part + (g * a.per_group + s) * 3 * a.C + c;
-                if (a.dscale) v[0] += p[0];
-                if (a.dscale || a.dshift) v[1] += p[a.C];
-                if (a.dgate) v[2] += p[2 * a.C];
+            for (int64_t s = s0 + y; s < s1; s += kJoinRows) {
+                const float* p = a.part + s * 3 * a.C + c;
+                if (a0) v[0] += p[0];
+                if (a1) v[1] += p[a.C];
+                if (a2) v[2] += p[2 * a.C];
             }
         }
-        join_rows(v, sh);
-        if (threadIdx.y == 0 && c < a.C) {
-            if (a.dscale) a.dscale[g * a.C + c] = fmaf(a.w ? a.w[c] : 1.f, v[0], a.b ? a.b[c] * v[1] : 0.f);
-            if (a.dshift) a.dshift[g * a.C + c] = v[1];
-            if (a.dgate) a.dgate[g * a.C + c] = a.w_post ? a.w_post[c] * v[2] : v[2];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) sh[y][i][x] = v[i];
+        __syncthreads();
+        if (y < 3) {
+            float s = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < kJoinRows; ++k) s += sh[k][y][x];
+            sums[y][x] = s;
         }
+        __syncthreads();
+        if (y == 0) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) v[i] = sums[i][x];
+        }
+    };
+    // v of the cluster's CTAs, added up in the first one
+    auto gather = [&](float (&v)[3]) {
+        if (n == 1) return;
+        __syncthreads();
+        if (y == 0) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) sums[i][x] = v[i];
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (me == 0) {
+            for (int q = y; q < 3 * (int)n; q += kJoinRows) {      // a warp each, so that they are under way together
+                const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&sums[q % 3][x]);
+                uint32_t there;
+                float f;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(q / 3));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(there) : "memory");
+                sh[q / 3][q % 3][x] = f;
+            }
+            __syncthreads();
+            if (y == 0)
+                for (int k = 1; k < (int)n; ++k)
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) v[i] += sh[k][i][x];
+        }
+        // no CTA overwrites its sums, or ends, while the first one reads them
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    };
+    float t[3] = {0.f, 0.f, 0.f};
+    auto group = [&](int64_t g, const float (&v)[3]) {
+        if (a.dscale) a.dscale[g * a.C + c] = fmaf(a.w ? a.w[c] : 1.f, v[0], a.b ? a.b[c] * v[1] : 0.f);
+        if (a.dshift) a.dshift[g * a.C + c] = v[1];
+        if (a.dgate) a.dgate[g * a.C + c] = a.w_post ? a.w_post[c] * v[2] : v[2];
+        const float one = a.scale ? 1.f + a.scale[g * a.ld_scale + c] : 1.f;
+        t[0] = fmaf(one, v[0], t[0]);
+        t[1] = fmaf(one, v[1], t[1]);
+        t[2] = fmaf(a.gate ? a.gate[g * a.ld_gate + c] : 1.f, v[2], t[2]);
+    };
+    float v[3];
+    if (a.per_group == 0) {
+        read(a.segs * me / n, a.segs * (me + 1) / n, t);
+        gather(t);
+    } else if (a.wide) {
+        for (int64_t g = 0; g < a.groups; ++g) {
+            const int64_t s0 = g * a.per_group;
+            read(s0 + a.per_group * me / n, s0 + a.per_group * (me + 1) / n, v);
+            gather(v);
+            if (me == 0 && y == 0 && in) group(g, v);
+        }
+    } else {
+        for (int64_t g = me; g < a.groups; g += n) {
+            read(g * a.per_group, (g + 1) * a.per_group, v);
+            if (y == 0 && in) group(g, v);
+        }
+        if (affine) gather(t);          // the same for all CTAs of the cluster
     }
+    if (me != 0 || y != 0 || !in) return;
+    if (a.dw) a.dw[c] = t[0];
+    if (a.db) a.db[c] = t[1];
+    if (a.dw_post) a.dw_post[c] = t[2];
 }
 
-__global__ void __launch_bounds__(512) k_block_norm_affine(const JoinArgs a) {
-    __shared__ float sh[16][3][32];
-    const int c = blockIdx.x * 32 + threadIdx.x;
-    const int64_t p0 = a.segs * blockIdx.y / gridDim.y, p1 = a.segs * (blockIdx.y + 1) / gridDim.y;
-    float v[3] = {0.f, 0.f, 0.f};
-    if (c < a.C) {
-#pragma unroll 4
-        for (int64_t s = p0 + threadIdx.y; s < p1; s += 16) {
-            const float* p = a.part + s * 3 * a.C + c;
-            const int64_t g = s / a.per_group;
-            const float one = a.scale ? 1.f + a.scale[g * a.ld_scale + c] : 1.f;
-            if (a.dw) v[0] = fmaf(one, p[0], v[0]);
-            if (a.db) v[1] = fmaf(one, p[a.C], v[1]);
-            if (a.dw_post) v[2] = fmaf(a.gate ? a.gate[g * a.ld_gate + c] : 1.f, p[2 * a.C], v[2]);
-        }
-    }
-    join_rows(v, sh);
-    if (threadIdx.y != 0 || c >= a.C) return;
-    if (gridDim.y > 1) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i) a.part2[((int64_t)blockIdx.y * 3 + i) * a.C + c] = v[i];
-        return;
-    }
-    if (a.dw) a.dw[c] = v[0];
-    if (a.db) a.db[c] = v[1];
-    if (a.dw_post) a.dw_post[c] = v[2];
-}
-
-__global__ void __launch_bounds__(512) k_block_norm_affine_join(const JoinArgs a, int n) {
-    __shared__ float sh[16][3][32];
-    const int c = blockIdx.x * 32 + threadIdx.x;
-    float v[3] = {0.f, 0.f, 0.f};
-    if (c < a.C) {
-        for (int s = threadIdx.y; s < n; s += 16)
-#pragma unroll
-            for (int i = 0; i < 3; ++i) v[i] += a.part2[((int64_t)s * 3 + i) * a.C + c];
-    }
-    join_rows(v, sh);
-    if (threadIdx.y != 0 || c >= a.C) return;
-    if (a.dw) a.dw[c] = v[0];
-    if (a.db) a.db[c] = v[1];
-    if (a.dw_post) a.dw_post[c] = v[2];
+static prism_status_t launch_join(JoinArgs j, cudaStream_t stream) {
+    // one group of 148 segments: 6 us by one CTA a column, 12 by a cluster; of 9472: 75 against 15
+    j.wide = j.groups <= 4 && j.per_group >= 512;
+    const int64_t parts = j.per_group == 0 || j.wide ? kMaxCluster : j.groups;
+    int n = 1;
+    while (n < kMaxCluster && 2 * n <= parts) n *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((j.C + 31) / 32), (unsigned)n);
+    cfg.blockDim = dim3(32, kJoinRows);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1;
+    at[0].val.clusterDim.y = (unsigned)n;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_block_norm_join, j) == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
 struct Split {
-    int64_t groups, per_group, segs;
+    int64_t groups, rpg, segs;
+    int per_group;               // segments a group; 0: a segment has whole groups
 };
 
-// Segments of rows, none across a group's end.  Where there are few groups, each is cut so that the
-// segments fill the teams that run at a time once; where groups are many, into about eight rounds of
-// such teams, so that the last round's idle part is small.  No segment below four rows is cut:
-// its column sums cost as much as three rows.
-static Split split_rows(const prism_block_norm_t* n) {
-    Split s{0, 1, 0};
+// Segments of rows.  Where there are few groups, each is cut so that the segments fill the teams that run at a time
+// once; where groups are many, into about eight rounds of such teams, so that the last round's idle part is small.
+// No segment below four rows (two where teams are left over) is cut: its column sums cost as much as three rows.  Groups that are not cut are shared
+// out in runs among the teams.
+static Split split_rows(const prism_block_norm_t* n, bool one_group) {
+    Split s{0, 1, 0, 0};
     if (n->rows == 0) return s;
-    const int64_t rpg = n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
-    s.groups = (n->rows + rpg - 1) / rpg;
+    s.rpg = !one_group && n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
+    s.groups = (n->rows + s.rpg - 1) / s.rpg;
     const int64_t teams = (int64_t)kSMs * sm_teams(n->channels, bwd_ctas(team_bucket(team_threads(n->channels))));
     int64_t per = s.groups * 4 <= teams ? teams / s.groups : 8 * teams / s.groups;
-    const int64_t most = (rpg + 3) / 4;
+    int64_t most = (s.rpg + 3) / 4;
+    if (s.groups * most < teams) most = (s.rpg + 1) / 2;      // little work: the shorter chain of rows counts more
     if (per > most) per = most;
-    if (per < 1) per = 1;
-    s.per_group = per;
-    s.segs = s.groups * s.per_group;
+    if (per > 1) {
+        s.per_group = (int)per;
+        s.segs = s.groups * per;
+    } else {
+        s.segs = s.groups < teams ? s.groups : teams;
+    }
     return s;
 }
+static int64_t part_floats(const Split& s, int C) { return s.segs * 3 * C; }
 
 static prism_status_t check(const prism_block_norm_t* n) {
     if (!n) return PRISM_ERR_INVALID_ARG;
@@ -170,7 +212,8 @@ extern "C" prism_status_t prism_block_norm_ws_bytes(const prism_block_norm_t* n,
     const prism_status_t st = check(n);
     if (st != PRISM_OK) return st;
     if (!bytes) return PRISM_ERR_INVALID_ARG;
-    *bytes = (size_t)(split_rows(n).segs + kMaxJoin) * 3 * n->channels * sizeof(float);
+    const int64_t a = part_floats(split_rows(n, false), n->channels), b = part_floats(split_rows(n, true), n->channels);
+    *bytes = (size_t)(a > b ? a : b) * sizeof(float);
     return PRISM_OK;
 }
 
@@ -243,19 +286,18 @@ extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, cons
     const int es = esize(n->stream_dtype), eb = esize(n->branch_dtype);
     if (!opt_on(dz, es) || (has_y && (!on(z, es) || !on(dy, eb))) || !on(dx, es) || (h && (!on(h, eb) || !on(dh, eb))))
         return PRISM_ERR_INVALID_ARG;
-    const Split s = split_rows(n);
-    const bool groups = dgate || dscale || dshift, affine = dw || db || dw_post, direct = s.per_group == 1;
-    const bool part = affine || (groups && !direct);
-    if (part && (!ws || ws_bytes < (size_t)(s.segs + kMaxJoin) * 3 * C * sizeof(float))) return PRISM_ERR_WORKSPACE;
-    if (s.segs > INT32_MAX) return PRISM_ERR_UNSUPPORTED;
+    // rows that share all their vectors are one group
+    const bool groups = dgate || dscale || dshift, affine = dw || db || dw_post;
+    const Split s = split_rows(n, !groups && !gate && !scale);
+    const bool part = affine || (groups && s.per_group > 0);
+    if (part && (!ws || ws_bytes < (size_t)part_floats(s, C) * sizeof(float))) return PRISM_ERR_WORKSPACE;
     a.z = z; a.h = h; a.dz = dz; a.dy = dy;
     a.gate = gate; a.w_post = w_post; a.w = w; a.b = b; a.scale = scale;
     a.dx = dx; a.dh = dh;
     a.part = part ? (float*)ws : nullptr;
-    if (direct) { a.dgate = dgate; a.dscale = dscale; a.dshift = dshift; }
+    if (s.per_group == 0) { a.dgate = dgate; a.dscale = dscale; a.dshift = dshift; }
     a.R = n->rows;
-    a.rpg = n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
-    a.segs = s.segs; a.per_group = (int)s.per_group;
+    a.rpg = s.rpg; a.groups = s.groups; a.segs = s.segs; a.per_group = s.per_group;
     a.C = C; a.norm = n->norm; a.post = n->post_norm; a.eps = n->eps; a.res = n->res_scale;
     const int unit = unit_of(C, {has_y ? a.ld_z : 0, h ? a.ld_h : 0, dz ? a.ld_dz : 0, has_y ? a.ld_dy : 0, a.ld_dx,
                                  h ? a.ld_dh : 0, gate ? a.ld_gate : 0, scale ? a.ld_scale : 0},
@@ -265,20 +307,10 @@ extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, cons
     else if (n->branch_dtype == PRISM_BF16) st = launch_bwd<float, __nv_bfloat16>(a, unit, stream);
     else st = launch_bwd<float, float>(a, unit, stream);
     if (st != PRISM_OK) return st;
-    int launches = 1;
-    JoinArgs j{(const float*)ws, w, b, w_post, scale, gate, dgate, dscale, dshift, dw, db, dw_post,
-               (float*)ws + s.segs * 3 * C, s.groups, s.segs, a.ld_scale, a.ld_gate, C, (int)s.per_group};
-    const unsigned gx = (unsigned)((C + 31) / 32);
-    if (groups && !direct) {
-        k_block_norm_groups<<<dim3(gx, (unsigned)(s.groups < 65535 ? s.groups : 65535)), dim3(32, 16), 0, stream>>>(j);
-        ++launches;
-    }
-    if (affine) {
-        int64_t n2 = s.segs / 64;
-        n2 = n2 < 1 ? 1 : n2 > kMaxJoin ? kMaxJoin : n2;
-        k_block_norm_affine<<<dim3(gx, (unsigned)n2), dim3(32, 16), 0, stream>>>(j);
-        if (n2 > 1) k_block_norm_affine_join<<<gx, dim3(32, 16), 0, stream>>>(j, (int)n2);
-        launches += n2 > 1 ? 2 : 1;
-    }
-    return launch_status(launches);
+    if (!part) return launch_status(1);
+    st = launch_join(JoinArgs{(const float*)ws, w, b, w_post, scale, gate, s.per_group ? dgate : nullptr,
+                              s.per_group ? dscale : nullptr, s.per_group ? dshift : nullptr, dw, db, dw_post, s.groups,
+                              s.segs, a.ld_scale, a.ld_gate, C, s.per_group, 0},
+                     stream);
+    return st == PRISM_OK ? launch_status(2) : st;
 }

@@ -43,17 +43,16 @@ struct BwdArgs {
     const void *z, *h, *dz, *dy;
     const float *gate, *w_post, *w, *b, *scale;
     void *dx, *dh;
-    // direct: each group is one segment and its gradients are written by the row kernel
-    float *dgate, *dscale, *dshift;
-    float* part;                       // [segments][3][C] column sums A, D, B; null: not wanted
-    int64_t R, rpg, segs;              // segs = groups x segments a group
+    float *dgate, *dscale, *dshift;    // [groups][C], where whole groups are a segment's; else null
+    float* part;                       // [segments][3][C] column sums; null: not wanted
+    int64_t R, rpg, groups, segs;
     int64_t ld_z, ld_h, ld_dz, ld_dy, ld_dx, ld_dh, ld_gate, ld_scale;
+    // segments a group; 0: a segment has whole groups, writes their gradients itself and leaves the sums over its
+    // groups that dw, db and dw_post are made of
     int C, norm, post, per_group;
     float eps, res;
 };
 
-// The threads of a team hold U units of E consecutive channels each: unit u of thread t covers
-// channels (u * threads + t) * E + [0, E), so that a warp's access to a unit is contiguous.
 template <int E> __device__ __forceinline__ void load_vec(float* f, const float* p) {
     if constexpr (E % 4 == 0) {
 #pragma unroll
@@ -66,6 +65,21 @@ template <int E> __device__ __forceinline__ void load_vec(float* f, const float*
         f[0] = v.x; f[1] = v.y;
     } else {
         f[0] = __ldg(p);
+    }
+}
+// what the same thread has written: not through the read-only path
+template <int E> __device__ __forceinline__ void load_own(float* f, const float* p) {
+    if constexpr (E % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            float4 v;
+            asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p + 4 * i) : "memory");
+            f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] = *(const volatile float*)(p + i);
     }
 }
 template <int E> __device__ __forceinline__ void store_vec(float* p, const float* f) {
@@ -235,7 +249,11 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fw
 // that lie on no wider boundary, through registers, one row ahead.
 extern __shared__ __align__(16) char g_ring[];
 
-// What the backward's branch is: none, one that goes to the sum as it is, or one with a norm of its own.
+constexpr bool vec_shared(int maxt) { return maxt > 640; }
+
+// What the backward's branch is: none, one that goes to the sum as it is, or one with a norm of its own.  (Behind an rms
+// norm of the branch mean(dn ∘ nh) can be put together from sums that are known before dz', one barrier a row less;
+// with its four more sums 8191 x 5120 took 127 us instead of 110.)
 enum Branch { kNoBranch = 0, kPlain = 1, kNormed = 2 };
 
 template <typename TX, typename TH, int E, int MAXT, int BR, int CTAS, int D>
@@ -251,10 +269,19 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
     const int t = threadIdx.x, T = blockDim.x, C = a.C;
     const int64_t seg = MAXT == 32 ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
     if (seg >= a.segs) return;
-    const int64_t g = seg / a.per_group;
-    // segment s of a group takes its rows s, s + per_group, ...: all teams move over the rows together
-    const int64_t r0 = g * a.rpg + (seg - g * a.per_group), step = a.per_group;
-    int64_t r1 = (g + 1) * a.rpg;
+    // Segment s of a group takes its rows s, s + per_group, ...: all teams move over the rows together.  Where groups
+    // are many and short a segment has a run of them.
+    int64_t g, r0, r1, step = 1;
+    if (a.per_group > 0) {
+        g = seg / a.per_group;
+        r0 = g * a.rpg + (seg - g * a.per_group);
+        r1 = (g + 1) * a.rpg;
+        step = a.per_group;
+    } else {
+        g = a.groups * seg / a.segs;
+        r0 = g * a.rpg;
+        r1 = a.groups * (seg + 1) / a.segs * a.rpg;
+    }
     if (r1 > a.R) r1 = a.R;
     const float fc = (float)C, inv_c = 1.f / fc;
     const bool has_y = a.norm != PRISM_NORM_NONE;
@@ -312,227 +339,288 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
 #pragma unroll
     for (int i = 0; i < (RING ? D : 1); ++i) fetch(r0 + i * step, i);
 
-    F2 mul[4], gate[HAS_H ? 4 : 1];
-    {
-        float m[8], q[8];
+    // The vectors stay in registers, or where these are too few (the widest teams) in shared memory behind the
+    // ring, read again for each use.
+    constexpr bool VSM = vec_shared(MAXT);
+    const uint32_t vec = (uint32_t)__cvta_generic_to_shared(g_ring) + (RING ? D * stage_bytes : 0) + tid * 16;
+    auto keep = [&](const F2 (&v)[4], int which) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = q[i] = 1.f;
+        for (int i = 0; i < 2; ++i)
+            asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(vec + (2 * which + i) * threads * 16), "l"(v[2 * i].v),
+                         "l"(v[2 * i + 1].v) : "memory");
+    };
+    auto get = [&](F2 (&v)[4], const F2 (&regs)[4], int which) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = (u * T + t) * E;
-            float s[E];
-            if (c < C) {
-                if (a.w) load_vec<E>(m + u * E, a.w + c);
-                if (a.scale) {
-                    load_vec<E>(s, a.scale + g * a.ld_scale + c);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) m[u * E + e] *= 1.f + s[e];
-                }
-                if (HAS_H) {
-                    if (a.gate) load_vec<E>(q + u * E, a.gate + g * a.ld_gate + c);
-                    if (a.w_post) {
-                        load_vec<E>(s, a.w_post + c);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) q[u * E + e] *= s[e];
-                    }
-                }
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (VSM) {
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[2 * i].v), "=l"(v[2 * i + 1].v)
+                             : "r"(vec + (2 * which + i) * threads * 16) : "memory");
+            } else {
+                v[2 * i] = regs[2 * i];
+                v[2 * i + 1] = regs[2 * i + 1];
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            mul[i] = f2(in(2 * i) ? m[2 * i] : 0.f, in(2 * i + 1) ? m[2 * i + 1] : 0.f);
-            if constexpr (HAS_H) gate[i] = f2(in(2 * i) ? q[2 * i] : 0.f, in(2 * i + 1) ? q[2 * i + 1] : 0.f);
-        }
-    }
-
-    F2 sA[4], sD[4], sB[HAS_H ? 4 : 1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sA[i] = sD[i] = f2(0.f);
-        if constexpr (HAS_H) sB[i] = f2(0.f);
-    }
-
+    };
     int stage = 0;
-    for (int64_t r = r0; r < r1; r += step) {
-        F2 z[4], dy[4], d[4], h[HAS_H ? 4 : 1];
-        if constexpr (RING) {
-            cp_wait<D - 1>();
-            const char* s = g_ring + stage * stage_bytes;
-            LX::read(z, s, threads, tid);
-            LH::read(dy, s + o_dy, threads, tid);
-            LX::read(d, s + o_dz, threads, tid);
-            if constexpr (HAS_H) LH::read(h, s + o_h, threads, tid);
-        } else {
+    bool first = true;
+    for (int64_t r = r0;;) {              // over the segment's groups
+        const int64_t end = a.per_group > 0 || (g + 1) * a.rpg > r1 ? r1 : (g + 1) * a.rpg;
+        F2 mul_[4], gate_[4];
+        {
+            float m[8], q[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f[2];
-                unpack<1>(rz[2 * i], f); unpack<1>(rz[2 * i + 1], f + 1);
-                z[i] = f2(f[0], f[1]);
-                unpack<1>(rdy[2 * i], f); unpack<1>(rdy[2 * i + 1], f + 1);
-                dy[i] = f2(f[0], f[1]);
-                unpack<1>(rdz[2 * i], f); unpack<1>(rdz[2 * i + 1], f + 1);
-                d[i] = f2(f[0], f[1]);
-                if constexpr (HAS_H) {
-                    unpack<1>(rh[2 * i], f); unpack<1>(rh[2 * i + 1], f + 1);
-                    h[i] = f2(f[0], f[1]);
-                }
-            }
-            fetch(r + step, 0);
-        }
-
-        // means first (layer): of z, of c = dy ∘ mul and of h
-        constexpr int NS = BR == kNormed ? 3 : 2;
-        float mc = 0.f;
-        if (a.norm == PRISM_NORM_LAYER || (BR == kNormed && a.post == PRISM_NORM_LAYER)) {
-            F2 q[3] = {z[0], dy[0] * mul[0], HAS_H ? h[0] : z[0]};
-#pragma unroll
-            for (int i = 1; i < 4; ++i) {
-                q[0] = q[0] + z[i];
-                q[1] = fma(dy[i], mul[i], q[1]);
-                if constexpr (BR == kNormed) q[2] = q[2] + h[i];
-            }
-            float s[NS];
-#pragma unroll
-            for (int i = 0; i < NS; ++i) s[i] = sum(q[i]);
-            team.sum(s);
-            if (a.norm == PRISM_NORM_LAYER) {
-                const float mz = -mean_of(s[0], fc, inv_c);
-                mc = s[1] * inv_c;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = z[i] + pair(mz, i);
-            }
-            if constexpr (BR == kNormed) {
-                if (a.post == PRISM_NORM_LAYER) {
-                    const float mh = -mean_of(s[NS - 1], fc, inv_c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = h[i] + pair(mh, i);
-                }
-            }
-        }
-        // second moments, and c against z
-        float rh_ = 1.f;
-        if (has_y || BR == kNormed) {
-            F2 q[3] = {z[0] * z[0], dy[0] * mul[0] * z[0], HAS_H ? h[0] * h[0] : z[0]};
-#pragma unroll
-            for (int i = 1; i < 4; ++i) {
-                q[0] = fma(z[i], z[i], q[0]);
-                q[1] = fma(dy[i] * mul[i], z[i], q[1]);
-                if constexpr (BR == kNormed) q[2] = fma(h[i], h[i], q[2]);
-            }
-            float s[NS];
-#pragma unroll
-            for (int i = 0; i < NS; ++i) s[i] = sum(q[i]);
-            team.sum(s);
-            if (has_y) {
-                const float rs = rsqrtf(s[0] * inv_c + a.eps), mcn = s[1] * rs * inv_c;
-                const F2 rs2 = f2(rs), mcn2 = f2(-mcn);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const F2 n = z[i] * rs2;
-                    sA[i] = fma(dy[i], n, sA[i]);
-                    sD[i] = sD[i] + dy[i];
-                    d[i] = fma(rs2, fma(n, mcn2, fma(dy[i], mul[i], pair(-mc, i))), d[i]);
-                }
-            }
-            if constexpr (BR == kNormed) rh_ = rsqrtf(s[NS - 1] * inv_c + a.eps);
-        }
-        auto put = [&](auto* row, const F2 (&v)[4]) {
-            using TO = typename std::remove_reference<decltype(*row)>::type;
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = both(v[i]);
-                o[2 * i] = f.x;
-                o[2 * i + 1] = f.y;
-            }
+            for (int i = 0; i < 8; ++i) m[i] = q[i] = 1.f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int c = (u * T + t) * E;
+                float s[E];
                 if (c < C) {
-                    Pack<TO, E> p;
-                    pack<E>(p, o + u * E);
-                    store(row + c, p);
+                    if (a.w) load_vec<E>(m + u * E, a.w + c);
+                    if (a.scale) {
+                        load_vec<E>(s, a.scale + g * a.ld_scale + c);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) m[u * E + e] *= 1.f + s[e];
+                    }
+                    if (HAS_H) {
+                        if (a.gate) load_vec<E>(q + u * E, a.gate + g * a.ld_gate + c);
+                        if (a.w_post) {
+                            load_vec<E>(s, a.w_post + c);
+#pragma unroll
+                            for (int e = 0; e < E; ++e) q[u * E + e] *= s[e];
+                        }
+                    }
                 }
             }
-        };
-        {
-            F2 o[4];
-            const F2 res = f2(HAS_H ? a.res : 1.f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = HAS_H ? d[i] * res : d[i];
-            put((TX*)a.dx + r * a.ld_dx, o);
-        }
-        if constexpr (HAS_H) {
-            F2 q[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if constexpr (BR == kNormed) h[i] = h[i] * f2(rh_);
-                sB[i] = fma(d[i], h[i], sB[i]);
-                d[i] = d[i] * gate[i];
+                mul_[i] = f2(in(2 * i) ? m[2 * i] : 0.f, in(2 * i + 1) ? m[2 * i + 1] : 0.f);
+                gate_[i] = f2(in(2 * i) ? q[2 * i] : 0.f, in(2 * i + 1) ? q[2 * i + 1] : 0.f);
+            }
+            if constexpr (VSM) {
+                keep(mul_, 0);
+                if constexpr (HAS_H) keep(gate_, 1);
+            }
+        }
+
+        F2 sA[4], sD[4], sB[HAS_H ? 4 : 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sA[i] = sD[i] = f2(0.f);
+            if constexpr (HAS_H) sB[i] = f2(0.f);
+        }
+
+        for (; r < end; r += step) {
+            F2 z[4], dy[4], d[4], h[HAS_H ? 4 : 1];
+            if constexpr (RING) {
+                cp_wait<D - 1>();
+                const char* s = g_ring + stage * stage_bytes;
+                LX::read(z, s, threads, tid);
+                LH::read(dy, s + o_dy, threads, tid);
+                LX::read(d, s + o_dz, threads, tid);
+                if constexpr (HAS_H) LH::read(h, s + o_h, threads, tid);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f[2];
+                    unpack<1>(rz[2 * i], f); unpack<1>(rz[2 * i + 1], f + 1);
+                    z[i] = f2(f[0], f[1]);
+                    unpack<1>(rdy[2 * i], f); unpack<1>(rdy[2 * i + 1], f + 1);
+                    dy[i] = f2(f[0], f[1]);
+                    unpack<1>(rdz[2 * i], f); unpack<1>(rdz[2 * i + 1], f + 1);
+                    d[i] = f2(f[0], f[1]);
+                    if constexpr (HAS_H) {
+                        unpack<1>(rh[2 * i], f); unpack<1>(rh[2 * i + 1], f + 1);
+                        h[i] = f2(f[0], f[1]);
+                    }
+                }
+                fetch(r + step, 0);
+            }
+
+            // means first (layer): of z, of c = dy ∘ mul and of h
+            constexpr int NS = BR == kNormed ? 3 : 2;
+            float mc = 0.f;
+            if (a.norm == PRISM_NORM_LAYER || (BR == kNormed && a.post == PRISM_NORM_LAYER)) {
+                F2 mul[4];
+                get(mul, mul_, 0);
+                F2 q[3] = {z[0], dy[0] * mul[0], HAS_H ? h[0] : z[0]};
+#pragma unroll
+                for (int i = 1; i < 4; ++i) {
+                    q[0] = q[0] + z[i];
+                    q[1] = fma(dy[i], mul[i], q[1]);
+                    if constexpr (BR == kNormed) q[2] = q[2] + h[i];
+                }
+                float s[NS];
+#pragma unroll
+                for (int i = 0; i < NS; ++i) s[i] = sum(q[i]);
+                team.sum(s);
+                if (a.norm == PRISM_NORM_LAYER) {
+                    const float mz = -mean_of(s[0], fc, inv_c);
+                    mc = s[1] * inv_c;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] = z[i] + pair(mz, i);
+                }
                 if constexpr (BR == kNormed) {
-                    q[0] = q[0] + d[i];
-                    q[1] = fma(d[i], h[i], q[1]);
+                    if (a.post == PRISM_NORM_LAYER) {
+                        const float mh = -mean_of(s[NS - 1], fc, inv_c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) h[i] = h[i] + pair(mh, i);
+                    }
                 }
             }
-            if constexpr (BR == kNormed) {
-                float s[2] = {sum(q[0]), sum(q[1])};
-                team.sum(s);
-                const F2 md = f2(a.post == PRISM_NORM_LAYER ? -s[0] * inv_c : 0.f), mdn = f2(-s[1] * inv_c), rr = f2(rh_);
+            // second moments, and c against z
+            float rh_ = 1.f;
+            if (has_y || BR == kNormed) {
+                F2 q[3], mul[4];
+                get(mul, mul_, 0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] = rr * fma(h[i], mdn, d[i] + md);
+                for (int i = 0; i < 4; ++i) {
+                    const F2 c = dy[i] * mul[i];
+                    q[0] = i ? fma(z[i], z[i], q[0]) : z[i] * z[i];
+                    q[1] = i ? fma(c, z[i], q[1]) : c * z[i];
+                    if constexpr (BR == kNormed) q[2] = i ? fma(h[i], h[i], q[2]) : h[i] * h[i];
+                }
+                float s[NS];
+#pragma unroll
+                for (int i = 0; i < NS; ++i) s[i] = sum(q[i]);
+                team.sum(s);
+                if constexpr (BR == kNormed) rh_ = rsqrtf(s[NS - 1] * inv_c + a.eps);
+                if (has_y) {
+                    const float rs = rsqrtf(s[0] * inv_c + a.eps), mcn = s[1] * rs * inv_c;
+                    const F2 rs2 = f2(rs), mcn2 = f2(-mcn);
+                    if constexpr (VSM) get(mul, mul_, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 n = z[i] * rs2;
+                        sA[i] = fma(dy[i], n, sA[i]);
+                        sD[i] = sD[i] + dy[i];
+                        d[i] = fma(rs2, fma(n, mcn2, fma(dy[i], mul[i], pair(-mc, i))), d[i]);
+                    }
+                }
             }
-            put((TH*)a.dh + r * a.ld_dh, d);
+            auto put = [&](auto* row, const F2 (&v)[4]) {
+                using TO = typename std::remove_reference<decltype(*row)>::type;
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = both(v[i]);
+                    o[2 * i] = f.x;
+                    o[2 * i + 1] = f.y;
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = (u * T + t) * E;
+                    if (c < C) {
+                        Pack<TO, E> p;
+                        pack<E>(p, o + u * E);
+                        store(row + c, p);
+                    }
+                }
+            };
+            {
+                F2 o[4];
+                const F2 res = f2(HAS_H ? a.res : 1.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = HAS_H ? d[i] * res : d[i];
+                put((TX*)a.dx + r * a.ld_dx, o);
+            }
+            if constexpr (HAS_H) {
+                F2 q[2], gate[4];
+                get(gate, gate_, 1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (BR == kNormed) h[i] = h[i] * f2(rh_);
+                    sB[i] = fma(d[i], h[i], sB[i]);
+                    d[i] = d[i] * gate[i];
+                    if constexpr (BR == kNormed) {
+                        q[0] = i ? q[0] + d[i] : d[i];
+                        q[1] = i ? fma(d[i], h[i], q[1]) : d[i] * h[i];
+                    }
+                }
+                if constexpr (BR == kNormed) {
+                    float s[2] = {sum(q[0]), sum(q[1])};
+                    team.sum(s);
+                    const F2 md = f2(a.post == PRISM_NORM_LAYER ? -s[0] * inv_c : 0.f), mdn = f2(-s[1] * inv_c), rr = f2(rh_);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = rr * fma(h[i], mdn, d[i] + md);
+                }
+                put((TH*)a.dh + r * a.ld_dh, d);
+            }
+            if constexpr (RING) {             // the row's own values have been used: their place is free
+                fetch(r + D * step, stage);
+                stage = stage + 1 == D ? 0 : stage + 1;
+            }
         }
-        if constexpr (RING) {             // the row's own values have been used: their place is free
-            fetch(r + D * step, stage);
-            stage = stage + 1 == D ? 0 : stage + 1;
+        float fA[8], fD[8], fB[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 f = both(sA[i]);
+            fA[2 * i] = f.x; fA[2 * i + 1] = f.y;
+            f = both(sD[i]);
+            fD[2 * i] = f.x; fD[2 * i + 1] = f.y;
+            f = both(sB[HAS_H ? i : 0]);
+            fB[2 * i] = f.x; fB[2 * i + 1] = f.y;
         }
+        const bool whole = a.per_group == 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = (u * T + t) * E;
+            if (c >= C) continue;
+            float w[E], b[E], f[E];
+            if (whole && (a.dscale || a.dshift || a.part)) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) { w[e] = 1.f; b[e] = f[e] = 0.f; }
+                if (a.dscale) {
+                    if (a.w) load_vec<E>(w, a.w + c);
+                    if (a.b) load_vec<E>(b, a.b + c);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) w[e] = fmaf(w[e], fA[u * E + e], b[e] * fD[u * E + e]);
+                    store_vec<E>(a.dscale + g * C + c, w);
+                }
+                if (a.dshift) store_vec<E>(a.dshift + g * C + c, fD + u * E);
+                if (a.scale) load_vec<E>(f, a.scale + g * a.ld_scale + c);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    fA[u * E + e] = fmaf(f[e], fA[u * E + e], fA[u * E + e]);
+                    fD[u * E + e] = fmaf(f[e], fD[u * E + e], fD[u * E + e]);
+                }
+            }
+            if constexpr (HAS_H) {
+                if (whole && (a.dgate || a.part)) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) w[e] = f[e] = 1.f;
+                    if (a.w_post) load_vec<E>(w, a.w_post + c);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) w[e] *= fB[u * E + e];
+                    if (a.dgate) store_vec<E>(a.dgate + g * C + c, w);
+                    if (a.gate) load_vec<E>(f, a.gate + g * a.ld_gate + c);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) fB[u * E + e] *= f[e];
+                }
+            }
+            if (a.part) {
+                // the thread's own places: a run of groups adds up there
+                float* p = a.part + seg * 3 * C + c;
+                if (!first) {
+                    load_own<E>(w, p);
+                    load_own<E>(b, p + C);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) { fA[u * E + e] += w[e]; fD[u * E + e] += b[e]; }
+                    if constexpr (HAS_H) {
+                        load_own<E>(w, p + 2 * C);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) fB[u * E + e] += w[e];
+                    }
+                }
+                store_vec<E>(p, fA + u * E);
+                store_vec<E>(p + C, fD + u * E);
+                if constexpr (HAS_H) store_vec<E>(p + 2 * C, fB + u * E);
+            }
+        }
+        if (end >= r1) break;
+        ++g;
+        first = false;
     }
     if constexpr (RING) cp_wait<0>();
-
-    float fA[8], fD[8], fB[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 f = both(sA[i]);
-        fA[2 * i] = f.x; fA[2 * i + 1] = f.y;
-        f = both(sD[i]);
-        fD[2 * i] = f.x; fD[2 * i + 1] = f.y;
-        f = both(sB[HAS_H ? i : 0]);
-        fB[2 * i] = f.x; fB[2 * i + 1] = f.y;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = (u * T + t) * E;
-        if (c >= C) continue;
-        if (a.part) {
-            float* p = a.part + seg * 3 * C + c;
-            store_vec<E>(p, fA + u * E);
-            store_vec<E>(p + C, fD + u * E);
-            if constexpr (HAS_H) store_vec<E>(p + 2 * C, fB + u * E);
-        }
-        if (a.dscale) {
-            float w[E], b[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) { w[e] = 1.f; b[e] = 0.f; }
-            if (a.w) load_vec<E>(w, a.w + c);
-            if (a.b) load_vec<E>(b, a.b + c);
-#pragma unroll
-            for (int e = 0; e < E; ++e) w[e] = fmaf(w[e], fA[u * E + e], b[e] * fD[u * E + e]);
-            store_vec<E>(a.dscale + g * C + c, w);
-        }
-        if (a.dshift) store_vec<E>(a.dshift + g * C + c, fD + u * E);
-        if constexpr (HAS_H) {
-            if (a.dgate) {
-                float w[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) w[e] = 1.f;
-                if (a.w_post) load_vec<E>(w, a.w_post + c);
-#pragma unroll
-                for (int e = 0; e < E; ++e) w[e] *= fB[u * E + e];
-                store_vec<E>(a.dgate + g * C + c, w);
-            }
-        }
-    }
 }
 
 // threads of a team: 8 channels a thread; 8, 16 or a whole number of warps
@@ -562,10 +650,11 @@ constexpr int kRowsAhead = 3;
 template <typename TX, typename TH, int E, int MAXT, int H>
 prism_status_t launch_bwd_one(const BwdArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
     constexpr int CTAS = bwd_ctas(MAXT), row = 8 * (int)(2 * sizeof(TX) + (H ? 2 : 1) * sizeof(TH));
-    constexpr int threads = MAXT == 32 ? 256 : MAXT;
-    constexpr int most = (200 << 10) / (row * threads * CTAS), D = most < 1 ? 1 : most > kRowsAhead ? kRowsAhead : most;
+    constexpr int threads = MAXT == 32 ? 256 : MAXT, vec = vec_shared(MAXT) ? (H ? 64 : 32) : 0;
+    constexpr int most = ((216 << 10) / CTAS - vec * threads) / (row * threads);
+    constexpr int D = most < 1 ? 1 : most > kRowsAhead ? kRowsAhead : most;
     auto kernel = &k_block_norm_bwd<TX, TH, E, MAXT, H, CTAS, D>;
-    const int bytes = Lane<TX, E>::kAsync && Lane<TH, E>::kAsync ? D * row * (int)(block.x * block.y) : 0;
+    const int bytes = ((Lane<TX, E>::kAsync && Lane<TH, E>::kAsync ? D * row : 0) + vec) * (int)(block.x * block.y);
     // with the static part, more than the 48 KB that need no leave
     if (bytes > 40 << 10 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return PRISM_ERR_CUDA;

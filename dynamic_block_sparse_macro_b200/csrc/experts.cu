@@ -23,8 +23,9 @@ using namespace rows;
 
 constexpr int kMaxTopK = 16, kMaxExperts = 1024, kMaxAlign = 4096;
 constexpr int kHist = 8192;                    // shared-memory counters: warps x experts
-constexpr int kOneCta = 8192;                  // slots that one CTA sorts alone
-constexpr int kTile = 4096;                    // slots a CTA at least, where several sort
+constexpr int kOneCta = 4096;                  // slots that one CTA sorts alone
+constexpr int kTile = 1024;                    // slots a CTA at least, where several sort
+constexpr int kBatch = 8;                      // ids of a lane that are on their way at a time
 
 struct PlanArgs {
     const void* ids;
@@ -58,16 +59,29 @@ __device__ __forceinline__ Runs runs_of(const PlanArgs& a) {
     return r;
 }
 
-__device__ __forceinline__ void count_runs(const PlanArgs& a, const Runs& r, int* hist) {
+// the experts of a lane's next kBatch slots from i on, 32 apart (-1: none)
+__device__ __forceinline__ void batch_of(const PlanArgs& a, int64_t i, int64_t end, int (&e)[kBatch]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) e[j] = expert_of(a, i + 32 * j + lane, end);
+}
+
+// e holds the run's first batch, and still does afterwards where the run has no more
+__device__ __forceinline__ void count_runs(const PlanArgs& a, const Runs& r, int* hist, int (&e)[kBatch]) {
+    batch_of(a, r.begin, r.end, e);
     for (int i = threadIdx.x; i < r.warps * a.E; i += blockDim.x) hist[i] = 0;
     __syncthreads();
     const int lane = threadIdx.x & 31;
     int* mine = hist + (threadIdx.x >> 5) * a.E;
-    for (int64_t i = r.begin; i < r.end; i += 32) {
-        const int e = expert_of(a, i + lane, r.end);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && (same & ((1u << lane) - 1)) == 0) mine[e] += __popc(same);
-        __syncwarp();
+    for (int64_t i = r.begin; i < r.end; i += 32 * kBatch) {
+        if (i > r.begin) batch_of(a, i, r.end, e);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (i + 32 * j >= r.end) break;
+            const unsigned same = __match_any_sync(0xffffffffu, e[j]);
+            if (e[j] >= 0 && (same & ((1u << lane) - 1)) == 0) mine[e[j]] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
 }
@@ -101,9 +115,11 @@ __device__ __forceinline__ int cta_scan(int v, int* sh, int* total) {
 __global__ void __launch_bounds__(1024) k_expert_count(const PlanArgs a) {
     __shared__ int hist[kHist];
     const Runs r = runs_of(a);
-    count_runs(a, r, hist);
+    int ids[kBatch];
+    count_runs(a, r, hist, ids);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         int s = 0;
+#pragma unroll 8
         for (int w = 0; w < r.warps; ++w) s += hist[w * a.E + e];
         a.ws[(int64_t)blockIdx.x * a.E + e] = s;
     }
@@ -117,7 +133,8 @@ __global__ void __launch_bounds__(1024) k_expert_place(const PlanArgs a) {
     const int E = a.E, tid = threadIdx.x;
     const Runs r = runs_of(a);
     for (int e = tid; e < E; e += 1024) before[e] = total[e] = 0;
-    count_runs(a, r, hist);
+    int ids[kBatch];
+    count_runs(a, r, hist, ids);
     if (gridDim.x > 1) {
         const int groups = 1024 / E, e = tid % E, gr = tid / E;
         if (gr < groups) {
@@ -158,17 +175,24 @@ __global__ void __launch_bounds__(1024) k_expert_place(const PlanArgs a) {
 
     const int lane = tid & 31;
     int* rank = hist + (tid >> 5) * E;
-    for (int64_t i = r.begin; i < r.end; i += 32) {
-        const int e = expert_of(a, i + lane, r.end);
-        const unsigned same = __match_any_sync(0xffffffffu, e), lower = same & ((1u << lane) - 1);
-        int row = -1;
-        if (e >= 0) row = before[e] + rank[e] + __popc(lower);
-        __syncwarp();
-        if (e >= 0 && lower == 0) rank[e] += __popc(same);
-        __syncwarp();
-        if (i + lane < r.end) {
-            a.pos[i + lane] = row;
-            if (row >= 0) a.src[row] = (int32_t)(i + lane);
+    const bool again = r.end - r.begin > 32 * kBatch;
+    for (int64_t i0 = r.begin; i0 < r.end; i0 += 32 * kBatch) {
+        if (again) batch_of(a, i0, r.end, ids);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t i = i0 + 32 * j;
+            if (i >= r.end) break;
+            const int e = ids[j];
+            const unsigned same = __match_any_sync(0xffffffffu, e), lower = same & ((1u << lane) - 1);
+            int row = -1;
+            if (e >= 0) row = before[e] + rank[e] + __popc(lower);
+            __syncwarp();
+            if (e >= 0 && lower == 0) rank[e] += __popc(same);
+            __syncwarp();
+            if (i + lane < r.end) {
+                a.pos[i + lane] = row;
+                if (row >= 0) a.src[row] = (int32_t)(i + lane);
+            }
         }
     }
     // rows without a slot: behind each expert's last one, and behind the last expert
@@ -246,8 +270,9 @@ template <typename T, int N> __global__ void __launch_bounds__(256) k_expert_dis
     }
 }
 
-template <typename T, int N> __global__ void __launch_bounds__(256) k_expert_combine(const MoveArgs a) {
-    constexpr int U = 2, J = 4;               // accesses a lane and choice, choices in flight
+// J choices at a time with U accesses of a lane each: eight on their way
+template <typename T, int N, int J> __global__ void __launch_bounds__(256) k_expert_combine(const MoveArgs a) {
+    constexpr int U = 8 / J;
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), t = item / a.segs;
     if (t >= a.R) return;
@@ -428,6 +453,17 @@ static bool ld_of(int64_t ld, int64_t C, int64_t* out) {
         }                                                                              \
     } while (0)
 
+template <int J> static void launch_combine(int dtype, int b, unsigned grid, cudaStream_t s, const MoveArgs& a) {
+    if (dtype == PRISM_BF16) {
+        if (b == 16) k_expert_combine<__nv_bfloat16, 8, J><<<grid, 256, 0, s>>>(a);
+        else if (b == 4) k_expert_combine<__nv_bfloat16, 2, J><<<grid, 256, 0, s>>>(a);
+        else k_expert_combine<__nv_bfloat16, 1, J><<<grid, 256, 0, s>>>(a);
+    } else {
+        if (b == 16) k_expert_combine<float, 4, J><<<grid, 256, 0, s>>>(a);
+        else k_expert_combine<float, 1, J><<<grid, 256, 0, s>>>(a);
+    }
+}
+
 template <int K> static void launch_bwd(int dtype, int b, unsigned grid, cudaStream_t s, const MoveArgs& a) {
     if (dtype == PRISM_BF16) {
         if (b == 16) k_expert_combine_bwd<__nv_bfloat16, 8, K><<<grid, 256, 0, s>>>(a);
@@ -516,10 +552,13 @@ extern "C" prism_status_t prism_expert_combine(const prism_experts_t* e, int32_t
     a.y = y; a.w = weights; a.add = add; a.out = out;
     const int b = unit_bytes(esz, channels, {a.ld_out, add ? a.ld_add : 0}, {y, add, out});
     a.units = (int)(channels * esz / b);
-    a.segs = (a.units + 63) / 64;
+    const int J = a.k <= 1 ? 1 : a.k <= 2 ? 2 : 4, lanes = 32 * (8 / J);
+    a.segs = (a.units + lanes - 1) / lanes;
     unsigned grid;
     if (!grid_of((a.R * a.segs + 7) / 8, false, 1, 0, &a, &grid)) return PRISM_ERR_UNSUPPORTED;
-    PRISM_EX_BY_UNIT(k_expert_combine, b, grid, stream, a);
+    if (J == 1) launch_combine<1>(dtype, b, grid, stream, a);
+    else if (J == 2) launch_combine<2>(dtype, b, grid, stream, a);
+    else launch_combine<4>(dtype, b, grid, stream, a);
     return launch_status(1);
 }
 

@@ -77,11 +77,14 @@ def test_norm_arguments_refused(L):
 def test_norm_workspace_grows_with_the_split_only(L):
     def size(**kw):
         return _abi.block_norm_ws_bytes(norm_desc(**kw))
-    # [segments + 64][3][C] floats; a row alone is one segment, and segments have four rows at least
-    assert size(rows=1) == 65 * 3 * 64 * 4
-    assert size(rows=8, rows_per_group=8) == 66 * 3 * 64 * 4
-    assert size(rows=10 ** 6, rows_per_group=10 ** 6) <= 5000 * 3 * 64 * 4
-    assert size(rows=1000, rows_per_group=1) == 1064 * 3 * 64 * 4
+    # [segments][3][C] floats; a row alone is one segment, and segments have two rows at least
+    assert size(rows=1) == 1 * 3 * 64 * 4
+    assert size(rows=8, rows_per_group=8) == 4 * 3 * 64 * 4
+    # 64 channels: teams of 8 threads, two CTAs of 32 teams an SM
+    assert size(rows=10 ** 6, rows_per_group=10 ** 6) == 148 * 64 * 3 * 64 * 4
+    # groups of one row are not cut, and shared out among the teams
+    assert size(rows=1000, rows_per_group=1) == 1000 * 3 * 64 * 4
+    assert size(rows=10 ** 5, rows_per_group=1) == 148 * 64 * 3 * 64 * 4
 
 
 def rot_desc(**kw):
@@ -165,7 +168,7 @@ def test_expert_sizes():
     assert _abi.expert_sizes(ex(rows=1, top_k=2, experts=64, align=128)) == (2 + 2 * 127, 0)
     assert _abi.expert_sizes(ex(rows=0)) == (0, 0)
     rows, ws = _abi.expert_sizes(ex(rows=61440, top_k=2, experts=16))
-    assert rows == 122880 and ws == -(-122880 // 4096) * 16 * 4
+    assert rows == 122880 and ws == -(-122880 // 1024) * 16 * 4
 
 
 def test_tensors_off_the_gpu_are_refused():

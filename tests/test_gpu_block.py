@@ -63,6 +63,15 @@ NORM_CASES = [
     (4099, 64, 1, BF16, BF16, "layer", None, "gate scale shift", 1.0),
     (3001, 72, 1500, BF16, BF16, None, "rms", "gate post_weight", 1.0),
     (2500, 128, 2500, F32, F32, "rms", None, "weight", 1.0),
+    # groups that are not cut, more of them than teams: runs of groups with all gradients
+    (10007, 64, 1, F32, F32, "layer", "rms", ALL, 1.0),
+    (1203, 2048, 2, BF16, BF16, "layer", "layer", ALL, 0.5),
+    (900, 1001, 1, BF16, BF16, "rms", "rms", ALL, 1.0),
+    # few groups, cut, on both sides of what one cluster's first CTA adds up, and many cut ones
+    (4000, 64, 1000, F32, BF16, "layer", None, ALL.replace("post_weight ", ""), 1.0),
+    (5000, 520, 1000, BF16, BF16, "layer", "rms", ALL, 1.0),
+    (20000, 40, 700, F32, F32, "rms", "layer", ALL, 1.0),
+    (40000, 96, 40000, BF16, BF16, "layer", "rms", ALL, 1.0),
 ]
 
 
@@ -390,8 +399,10 @@ EXPERT_CASES = [
     (33, 16, 16, 100, F32, 3, 0.2, torch.int64),
     (700, 2, 1024, 64, BF16, 8, 0.0, torch.int32),
     (2049, 3, 7, 333, F32, 4, 0.2, torch.int64),
-    (2731, 3, 5, 72, BF16, 16, 0.0, torch.int64),       # 8193 slots: one more than one CTA sorts
+    (2731, 3, 5, 72, BF16, 16, 0.0, torch.int64),       # 8193 slots
     (8192, 1, 9, 40, BF16, 1, 0.0, torch.int64),
+    (4096, 1, 300, 24, F32, 2, 0.0, torch.int32),       # as many slots as one CTA sorts
+    (4097, 1, 300, 24, F32, 2, 0.1, torch.int32),
     (20000, 8, 128, 48, BF16, 128, 0.1, torch.int64),
     (31, 9, 12, 2048, F32, 1, 0.0, torch.int64),
     (77777, 2, 1000, 8, F32, 1, 0.0, torch.int32),
@@ -439,6 +450,27 @@ def test_experts_there_and_back(R, k, E, C, dt, align, dropped, idt):
     # in place of ys
     dys3, _ = block.expert_combine_backward(dout, ys, plan, w, out=ys)
     assert torch.equal(dys3[:used], dys[:used])
+
+
+def test_expert_plan_of_runs_longer_than_a_batch():
+    """More slots than 148 CTAs take at eight a thread: 1.3 million and odd."""
+    R, k, E = 650011, 2, 40
+    ids = torch.randint(-1, E, (R, k), device="cuda", generator=torch.Generator("cuda").manual_seed(5))
+    plan = block.expert_plan(ids, E, align=8)
+    flat = ids.view(-1)
+    key = torch.where(flat < 0, torch.full_like(flat, E), flat)
+    order = torch.sort(key, stable=True).indices
+    counts = torch.bincount(key, minlength=E + 1)[:E]
+    assert torch.equal(plan.counts.long(), counts)
+    offsets = torch.cumsum((counts + 7) // 8 * 8, 0)
+    assert torch.equal(plan.offsets[1:].long(), offsets) and int(plan.offsets[0]) == 0
+    used = plan.src[plan.src >= 0].long()
+    assert torch.equal(used, order[:int(counts.sum())])           # stable, expert by expert
+    there = plan.pos.view(-1) >= 0
+    assert torch.equal(there, flat >= 0)
+    slots = torch.nonzero(there).view(-1)
+    assert torch.equal(plan.src[plan.pos.view(-1)[slots].long()].long(), slots)
+    assert int((plan.src >= 0).sum()) == int(counts.sum())
 
 
 @pytest.mark.parametrize("align", [1, 16])
