@@ -607,7 +607,7 @@ class ExpertPlan:
     offsets[experts] are in use.
     """
     __slots__ = ("rows", "top_k", "experts", "align", "device", "rows_sorted", "counts", "offsets", "pos", "src",
-                 "_call", "_all", "_ws")
+                 "_call")
 
     def __init__(self, rows, top_k, experts, align, id_bytes, device):
         key = ("experts", rows, top_k, experts, align, id_bytes, device)
@@ -615,14 +615,14 @@ class ExpertPlan:
         if p is None:
             p = _Plan(_abi.ExpertsT(rows, top_k, experts, align, id_bytes), device)
             p.a, p.ws_bytes = _abi.expert_sizes(p.desc)
-            p.b = (experts, experts + 1, rows * top_k, p.a, p.ws_bytes // 4)
-            p.c = sum(p.b)
             _keep(key, p)
         self._call, self.rows_sorted = p, p.a
         self.rows, self.top_k, self.experts, self.align, self.device = rows, top_k, experts, align, device
-        self._all = torch.empty(p.c, dtype=torch.int32, device=device)
-        self.counts, self.offsets, pos, self.src, self._ws = self._all.split_with_sizes(p.b)
-        self.pos = pos.view(rows, top_k)
+        e = torch.empty
+        self.counts = e(experts, dtype=torch.int32, device=device)
+        self.offsets = e(experts + 1, dtype=torch.int32, device=device)
+        self.pos = e(rows, top_k, dtype=torch.int32, device=device)
+        self.src = e(p.a, dtype=torch.int32, device=device)
 
 
 def expert_plan(ids, experts, align=1) -> ExpertPlan:
@@ -640,10 +640,21 @@ def expert_plan(ids, experts, align=1) -> ExpertPlan:
     rows, top_k = ids.shape
     p = ExpertPlan(rows, top_k, int(experts), int(align), ids.element_size(), dev)
     c = p._call
-    _check("prism_expert_plan", _abi.lib().prism_expert_plan(
-        c.addr, ids.data_ptr(), p.counts.data_ptr(), p.offsets.data_ptr(), p.pos.data_ptr(), p.src.data_ptr(),
-        p._ws.data_ptr() if c.ws_bytes else None, c.ws_bytes, _stream(dev.index)))
+    ws = torch.empty(c.ws_bytes, dtype=torch.uint8, device=dev) if c.ws_bytes else None
+    code = _abi.lib().prism_expert_plan(c.addr, ids.data_ptr(), p.counts.data_ptr(), p.offsets.data_ptr(),
+                                        p.pos.data_ptr(), p.src.data_ptr(), _ptr(ws),
+                                        c.ws_bytes, _stream(dev.index))
+    if code:
+        raise _abi.PrismError("prism_expert_plan", code)
     return p
+
+
+def _extent(t):
+    """Bytes from a tensor's first element to its last one's end."""
+    if t is None or not t.numel():
+        return 0
+    a, b = _bytes(t)
+    return b - a
 
 
 def _by_token(t, plan, C, dtype, what):
@@ -684,21 +695,23 @@ def expert_dispatch(x, plan, *, out=None):
         _sorted(out, plan, x.shape[1], x.dtype, "out")
         _need(out is None or out.is_contiguous(), "out must be dense")
         p = _keep(key, _Plan(call.desc, plan.device, ld is None))
-        p.a = (_DT[x.dtype], x.shape[1], ld)
+        p.a = (_DT[x.dtype], x.shape[1], ld, _extent(x), _extent(out))
     if p.copy:
         return expert_dispatch(x.contiguous(), plan, out=out)
     if not _current(p.index):
         with torch.cuda.device(p.index):
             return expert_dispatch(x, plan, out=out)
-    dt, C, ld = p.a
+    dt, C, ld, n_x, n_out = p.a
     clear = out is None
     if clear:
         out = torch.empty(plan.rows_sorted, C, dtype=x.dtype, device=x.device)
-    else:
-        _check_out(out, "out", None, x, plan._all)
-    _check("prism_expert_dispatch", _abi.lib().prism_expert_dispatch(
-        p.addr, dt, C, x.data_ptr(), ld, plan.pos.data_ptr(), plan.counts.data_ptr(), plan.offsets.data_ptr(), clear,
-        out.data_ptr(), _stream(p.index)))
+    p_x, p_out = x.data_ptr(), out.data_ptr()
+    if p_x < p_out + n_out and p_out < p_x + n_x:
+        _check_out(out, "out", None, x)
+    code = _abi.lib().prism_expert_dispatch(p.addr, dt, C, p_x, ld, plan.pos.data_ptr(), plan.counts.data_ptr(),
+                                            plan.offsets.data_ptr(), clear, p_out, _stream(p.index))
+    if code:
+        raise _abi.PrismError("prism_expert_dispatch", code)
     return out
 
 
@@ -728,10 +741,13 @@ def expert_combine(ys, plan, weights=None, *, add=None, out=None):
     if out is None:
         out = torch.empty(plan.rows, C, dtype=ys.dtype, device=ys.device)
     else:
-        _check_out(out, "out", add, ys, weights, plan._all)
-    _check("prism_expert_combine", _abi.lib().prism_expert_combine(
-        p.addr, dt, C, ys.data_ptr(), plan.pos.data_ptr(), _ptr(weights), _ptr(add), ld_add, out.data_ptr(), ld_out,
-        _stream(p.index)))
+        _check_out(out, "out", add, ys, weights)
+    code = _abi.lib().prism_expert_combine(p.addr, dt, C, ys.data_ptr(), plan.pos.data_ptr(),
+                                           _ptr(weights),
+                                           _ptr(add), ld_add, out.data_ptr(), ld_out,
+                                           _stream(p.index))
+    if code:
+        raise _abi.PrismError("prism_expert_combine", code)
     return out
 
 
@@ -754,7 +770,7 @@ def expert_combine_backward(dout, ys, plan, weights=None, *, out=None, want_weig
         _need(out is None or out.is_contiguous(), "out must be dense")
         p = _keep(key, _Plan(call.desc, plan.device, ld is None or (ys is not None and not ys.is_contiguous())
                              or (weights is not None and not weights.is_contiguous())))
-        p.a = (_DT[dout.dtype], C, ld)
+        p.a = (_DT[dout.dtype], C, ld, _extent(out), _extent(ys), _extent(dout), _extent(weights))
     if p.copy:
         return expert_combine_backward(_dense(dout), None if ys is None else ys.contiguous(), plan,
                                        None if weights is None else weights.contiguous(), out=out,
@@ -762,18 +778,29 @@ def expert_combine_backward(dout, ys, plan, weights=None, *, out=None, want_weig
     if not _current(p.index):
         with torch.cuda.device(p.index):
             return expert_combine_backward(dout, ys, plan, weights, out=out, want_weights=want_weights)
-    dt, C, ld = p.a
+    dt, C, ld, n_out, n_y, n_d, n_w = p.a
+    p_d = dout.data_ptr()
+    p_y = _ptr(ys)
+    p_w = _ptr(weights)
     clear = out is None
     if clear:
         out = torch.empty(plan.rows_sorted, C, dtype=dout.dtype, device=dout.device)
+        p_out = out.data_ptr()
     else:
-        _check_out(out, "out", ys, dout, weights, plan._all)
-    dw = None
+        p_out = out.data_ptr()
+        end = p_out + n_out
+        if (p_d < end and p_out < p_d + n_d or p_y is not None and p_y < end and p_out < p_y + n_y
+                or p_w is not None and p_w < end and p_out < p_w + n_w):
+            _check_out(out, "out", ys, dout, weights)
+    dw = p_dw = None
     if want_weights:
         dw = torch.empty(plan.rows, plan.top_k, dtype=torch.float32, device=dout.device)
-    _check("prism_expert_combine_bwd", _abi.lib().prism_expert_combine_bwd(
-        p.addr, dt, C, dout.data_ptr(), ld, _ptr(ys), plan.pos.data_ptr(), _ptr(weights), plan.counts.data_ptr(),
-        plan.offsets.data_ptr(), clear, out.data_ptr(), _ptr(dw), _stream(p.index)))
+        p_dw = dw.data_ptr()
+    code = _abi.lib().prism_expert_combine_bwd(p.addr, dt, C, p_d, ld, p_y, plan.pos.data_ptr(), p_w,
+                                               plan.counts.data_ptr(), plan.offsets.data_ptr(), clear, p_out, p_dw,
+                                               _stream(p.index))
+    if code:
+        raise _abi.PrismError("prism_expert_combine_bwd", code)
     return out, dw
 
 

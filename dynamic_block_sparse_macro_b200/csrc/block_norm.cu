@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) k_block_norm_join(const JoinAr
     const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * 32 + x;
     const bool in = c < a.C, affine = a.dw || a.db || a.dw_post;
     const int64_t n = gridDim.y, me = blockIdx.y;
+    wait_for_previous();
     // v: the sums over the segments s0, s0 + 1, ... s1 - 1, in the threads y = 0
     auto read = [&](int64_t s0, int64_t s1, float (&v)[3]) {
         v[0] = v[1] = v[2] = 0.f;
@@ -130,18 +131,8 @@ static prism_status_t launch_join(JoinArgs j, cudaStream_t stream) {
     const int64_t parts = j.per_group == 0 || j.wide ? kMaxCluster : j.groups;
     int n = 1;
     while (n < kMaxCluster && 2 * n <= parts) n *= 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((j.C + 31) / 32), (unsigned)n);
-    cfg.blockDim = dim3(32, kJoinRows);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1;
-    at[0].val.clusterDim.y = (unsigned)n;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_block_norm_join, j) == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
+    return launch_after(k_block_norm_join, dim3((unsigned)((j.C + 31) / 32), (unsigned)n), dim3(32, kJoinRows), n, stream, j)
+               ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
 struct Split {

@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
         first = false;
     }
     if constexpr (RING) cp_wait<0>();
+    let_next_start();
 }
 
 // threads of a team: 8 channels a thread; 8, 16 or a whole number of warps

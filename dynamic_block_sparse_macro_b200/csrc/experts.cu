@@ -23,7 +23,7 @@ using namespace rows;
 
 constexpr int kMaxTopK = 16, kMaxExperts = 1024, kMaxAlign = 4096;
 constexpr int kHist = 8192;                    // shared-memory counters: warps x experts
-constexpr int kOneCta = 4096;                  // slots that one CTA sorts alone
+constexpr int kOneCta = 2048;                  // slots that one CTA sorts alone
 constexpr int kTile = 1024;                    // slots a CTA at least, where several sort
 constexpr int kBatch = 8;                      // ids of a lane that are on their way at a time
 
@@ -114,6 +114,7 @@ __device__ __forceinline__ int cta_scan(int v, int* sh, int* total) {
 // Where several CTAs sort: each CTA's counts.
 __global__ void __launch_bounds__(1024) k_expert_count(const PlanArgs a) {
     __shared__ int hist[kHist];
+    let_next_start();
     const Runs r = runs_of(a);
     int ids[kBatch];
     count_runs(a, r, hist, ids);
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(1024) k_expert_count(const PlanArgs a) {
 // Ranks and rows.  A slot's row = its expert's offset + the expert's slots in earlier CTAs, earlier warps of
 // this CTA and earlier lanes.  Every CTA sums the counts of all CTAs itself (a few hundred KB from L2), which
 // takes less time than a launch of its own for it.
-__global__ void __launch_bounds__(1024) k_expert_place(const PlanArgs a) {
+__global__ void __launch_bounds__(1024, 2) k_expert_place(const PlanArgs a) {
     __shared__ int hist[kHist], before[kMaxExperts], total[kMaxExperts], sh[32];
     const int E = a.E, tid = threadIdx.x;
     const Runs r = runs_of(a);
@@ -136,12 +137,13 @@ __global__ void __launch_bounds__(1024) k_expert_place(const PlanArgs a) {
     int ids[kBatch];
     count_runs(a, r, hist, ids);
     if (gridDim.x > 1) {
+        wait_for_previous();             // the counts of all CTAs, and what was in the outputs before
         const int groups = 1024 / E, e = tid % E, gr = tid / E;
         if (gr < groups) {
             int p = 0, t = 0;
 #pragma unroll 8
             for (int b = gr; b < (int)gridDim.x; b += groups) {
-                const int c = __ldg(a.ws + (int64_t)b * E + e);
+                const int c = a.ws[(int64_t)b * E + e];
                 t += c;
                 if (b < (int)blockIdx.x) p += c;
             }
@@ -270,30 +272,21 @@ template <typename T, int N> __global__ void __launch_bounds__(256) k_expert_dis
     }
 }
 
-// J choices at a time with U accesses of a lane each: eight on their way
-template <typename T, int N, int J> __global__ void __launch_bounds__(256) k_expert_combine(const MoveArgs a) {
+// J choices at a time with U accesses of a lane each, eight on their way; ALL: there are no more than J choices, and
+// each access is summed and stored by itself.
+template <typename T, int N, int J, bool ALL> __global__ void __launch_bounds__(256) k_expert_combine(const MoveArgs a) {
     constexpr int U = 8 / J;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), t = item / a.segs;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+    const int64_t item = (int64_t)blockIdx.x * 8 + warp, t = item / a.segs;
     if (t >= a.R) return;
     const int u0 = (int)(item - t * a.segs) * (32 * U) + lane;
     const int64_t p = token_pos(a, t, lane);
     const float w = a.w && lane < a.k ? __ldg(a.w + t * a.k + lane) : 1.f;
-    float s[U * N];
-#pragma unroll
-    for (int i = 0; i < U * N; ++i) s[i] = 0.f;
-    if (a.add) {
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (u0 + 32 * i < a.units) {
-                Pack<T, N> v;
-                load(v, (const T*)a.add + t * a.ld_add + (u0 + 32 * i) * N);
-                unpack<N>(v, s + i * N);
-            }
-    }
-    for (int j0 = 0; j0 < a.k; j0 += J) {
-        Pack<T, N> v[J][U];
-        int64_t row[J];
+    const T* add = a.add ? (const T*)a.add + t * a.ld_add : nullptr;
+    T* out = (T*)a.out + t * a.ld_out;
+    Pack<T, N> v[J][U];
+    int64_t row[J];
+    auto fetch = [&](int j0) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             row[j] = __shfl_sync(0xffffffffu, p, (j0 + j) & 31);
@@ -304,27 +297,64 @@ template <typename T, int N, int J> __global__ void __launch_bounds__(256) k_exp
                     if (u0 + 32 * i < a.units) load(v[j][i], (const T*)a.y + row[j] * a.C + (u0 + 32 * i) * N);
             }
         }
+    };
+    auto start = [&](int i, float* s) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-            if (row[j] < 0) continue;             // a dropped choice's weight, NaN or not, is not used
+        for (int e = 0; e < N; ++e) s[e] = 0.f;
+        if (add && u0 + 32 * i < a.units) {
+            Pack<T, N> q;
+            load(q, add + (u0 + 32 * i) * N);
+            unpack<N>(q, s);
+        }
+    };
+    auto finish = [&](int i, const float* s) {
+        if (u0 + 32 * i < a.units) {
+            Pack<T, N> q;
+            pack<N>(q, s);
+            store(out + (u0 + 32 * i) * N, q);
+        }
+    };
+    if constexpr (ALL) {
+        fetch(0);
+        float wj[J];
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (u0 + 32 * i < a.units) {
+        for (int j = 0; j < J; ++j) wj[j] = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float s[N];
+            start(i, s);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (row[j] >= 0) {                        // a dropped choice's weight, NaN or not, is not used
                     float f[N];
                     unpack<N>(v[j][i], f);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) s[i * N + e] = fmaf(wj, f[e], s[i * N + e]);
+                    for (int e = 0; e < N; ++e) s[e] = fmaf(wj[j], f[e], s[e]);
                 }
+            finish(i, s);
         }
-    }
+    } else {
+        float s[U][N];
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-        if (u0 + 32 * i < a.units) {
-            Pack<T, N> v;
-            pack<N>(v, s + i * N);
-            store((T*)a.out + t * a.ld_out + (u0 + 32 * i) * N, v);
+        for (int i = 0; i < U; ++i) start(i, s[i]);
+        for (int j0 = 0; j0 < a.k; j0 += J) {
+            fetch(j0);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+                if (row[j] < 0) continue;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    float f[N];
+                    unpack<N>(v[j][i], f);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) s[i][e] = fmaf(wj, f[e], s[i][e]);
+                }
+            }
         }
+#pragma unroll
+        for (int i = 0; i < U; ++i) finish(i, s[i]);
+    }
 }
 
 // segs warps of a CTA share a token; K >= k choices, whose dot products stay in registers
@@ -453,14 +483,14 @@ static bool ld_of(int64_t ld, int64_t C, int64_t* out) {
         }                                                                              \
     } while (0)
 
-template <int J> static void launch_combine(int dtype, int b, unsigned grid, cudaStream_t s, const MoveArgs& a) {
+template <int J, bool ALL> static void launch_combine(int dtype, int b, unsigned grid, cudaStream_t s, const MoveArgs& a) {
     if (dtype == PRISM_BF16) {
-        if (b == 16) k_expert_combine<__nv_bfloat16, 8, J><<<grid, 256, 0, s>>>(a);
-        else if (b == 4) k_expert_combine<__nv_bfloat16, 2, J><<<grid, 256, 0, s>>>(a);
-        else k_expert_combine<__nv_bfloat16, 1, J><<<grid, 256, 0, s>>>(a);
+        if (b == 16) k_expert_combine<__nv_bfloat16, 8, J, ALL><<<grid, 256, 0, s>>>(a);
+        else if (b == 4) k_expert_combine<__nv_bfloat16, 2, J, ALL><<<grid, 256, 0, s>>>(a);
+        else k_expert_combine<__nv_bfloat16, 1, J, ALL><<<grid, 256, 0, s>>>(a);
     } else {
-        if (b == 16) k_expert_combine<float, 4, J><<<grid, 256, 0, s>>>(a);
-        else k_expert_combine<float, 1, J><<<grid, 256, 0, s>>>(a);
+        if (b == 16) k_expert_combine<float, 4, J, ALL><<<grid, 256, 0, s>>>(a);
+        else k_expert_combine<float, 1, J, ALL><<<grid, 256, 0, s>>>(a);
     }
 }
 
@@ -511,9 +541,13 @@ extern "C" prism_status_t prism_expert_plan(const prism_experts_t* e, const void
     if (ctas > 1 && (!ws || ws_bytes < (size_t)ctas * e->experts * sizeof(int32_t))) return PRISM_ERR_WORKSPACE;
     const PlanArgs a{ids, counts, offsets, pos, src, (int32_t*)ws, e->rows * e->top_k, capacity(e),
                      e->experts, e->align, e->id_bytes, tile_of(e)};
-    if (ctas > 1) k_expert_count<<<(unsigned)ctas, 1024, 0, stream>>>(a);
-    k_expert_place<<<(unsigned)ctas, 1024, 0, stream>>>(a);
-    return launch_status(ctas > 1 ? 2 : 1);
+    if (ctas == 1) {
+        k_expert_place<<<1, 1024, 0, stream>>>(a);
+        return launch_status(1);
+    }
+    k_expert_count<<<(unsigned)ctas, 1024, 0, stream>>>(a);
+    if (!launch_after(k_expert_place, dim3((unsigned)ctas), dim3(1024), 1, stream, a)) return PRISM_ERR_CUDA;
+    return launch_status(2);
 }
 
 extern "C" prism_status_t prism_expert_dispatch(const prism_experts_t* e, int32_t dtype, int64_t channels, const void* x,
@@ -556,9 +590,10 @@ extern "C" prism_status_t prism_expert_combine(const prism_experts_t* e, int32_t
     a.segs = (a.units + lanes - 1) / lanes;
     unsigned grid;
     if (!grid_of((a.R * a.segs + 7) / 8, false, 1, 0, &a, &grid)) return PRISM_ERR_UNSUPPORTED;
-    if (J == 1) launch_combine<1>(dtype, b, grid, stream, a);
-    else if (J == 2) launch_combine<2>(dtype, b, grid, stream, a);
-    else launch_combine<4>(dtype, b, grid, stream, a);
+    if (J == 1) launch_combine<1, true>(dtype, b, grid, stream, a);
+    else if (J == 2) launch_combine<2, true>(dtype, b, grid, stream, a);
+    else if (a.k <= 4) launch_combine<4, true>(dtype, b, grid, stream, a);
+    else launch_combine<4, false>(dtype, b, grid, stream, a);
     return launch_status(1);
 }
 

@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
         }
     }
     if constexpr (BWD) {
+        let_next_start();
         if (!a.part) return;
         __shared__ float sh[256 / LPH][D];
         const int team = threadIdx.x / LPH;
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(512) k_head_rotate_join(const float* part, int
     __shared__ float sh[16][32];
     const int c = blockIdx.x * 32 + threadIdx.x;
     float* dw = blockIdx.y ? dwk : dwq;
+    wait_for_previous();
     float s = 0.f;
 #pragma unroll 4
     for (int i = threadIdx.y; i < n; i += 16) s += part[((int64_t)blockIdx.y * n + i) * D + c];
@@ -403,9 +405,11 @@ static prism_status_t rotate(const prism_rotate_t* p, const void* Q, const void*
         a.part = (float*)ws;
     }
     launch<true>(p, a, grid, stream);
-    if (dw)
-        k_head_rotate_join<<<dim3(p->head_dim / 32, sides), dim3(32, 16), 0, stream>>>(
-            a.part, (int)ctas, p->head_dim, hq ? dwq : dwk, hq ? dwk : nullptr);
+    if (dw) {
+        if (!launch_after(k_head_rotate_join, dim3(p->head_dim / 32, sides), dim3(32, 16), 1, stream, (const float*)a.part,
+                          (int)ctas, (int)p->head_dim, hq ? dwq : dwk, hq ? dwk : (float*)nullptr))
+            return PRISM_ERR_CUDA;
+    }
     return launch_status(dw ? 2 : 1);
 }
 

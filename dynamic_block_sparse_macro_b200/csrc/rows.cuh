@@ -21,6 +21,28 @@ struct Bits {
 inline bool on(const void* p, int b) { return p != nullptr && (uintptr_t)p % b == 0; }
 inline bool opt_on(const void* p, int b) { return (uintptr_t)p % b == 0; }
 
+// A kernel that finishes another one's work is launched while that one runs and waits for it where it first needs
+// its results, so that its start is not waited for.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... A>
+inline bool launch_after(void (*kernel)(A...), dim3 grid, dim3 block, int cluster_y, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = (unsigned)cluster_y;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster_y > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
 // N consecutive elements of T as they lie in memory
 template <typename T, int N> struct Pack {
     static constexpr int kBytes = (int)sizeof(T) * N;
