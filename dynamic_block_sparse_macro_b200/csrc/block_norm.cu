@@ -150,7 +150,8 @@ static Split split_rows(const prism_block_norm_t* n, bool one_group) {
     s.rpg = !one_group && n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
     s.groups = (n->rows + s.rpg - 1) / s.rpg;
     const int64_t teams = (int64_t)kSMs * sm_teams(n->channels, bwd_ctas(team_bucket(team_threads(n->channels))));
-    int64_t per = s.groups * 4 <= teams ? teams / s.groups : 8 * teams / s.groups;
+    // of the teams a group's share by its rows: the last group may be shorter than the others
+    int64_t per = (s.groups * 4 <= teams ? teams : 8 * teams) * s.rpg / n->rows;
     int64_t most = (s.rpg + 3) / 4;
     if (s.groups * most < teams) most = (s.rpg + 1) / 2;      // little work: the shorter chain of rows counts more
     if (per > most) per = most;
@@ -184,12 +185,12 @@ static bool ld_of(int64_t ld, int C, int64_t* out) {
 }
 
 // channels an access may take: all strides in use and the width are multiples of it, and all addresses of its bytes
-static int unit_of(int C, std::initializer_list<int64_t> lds, std::initializer_list<const void*> ptrs) {
+static int unit_of(int wide, int C, std::initializer_list<int64_t> lds, std::initializer_list<const void*> ptrs) {
     Bits n, p;
     n.bytes(C);
     for (int64_t l : lds) n.bytes(l);
     for (const void* q : ptrs) p << q;
-    return n.multiple_of(8) && p.multiple_of(16) ? 8 : n.multiple_of(2) && p.multiple_of(8) ? 2 : 1;
+    return n.multiple_of(wide) && p.multiple_of(16) ? wide : n.multiple_of(2) && p.multiple_of(8) ? 2 : 1;
 }
 static int esize(int dtype) { return dtype == PRISM_BF16 ? 2 : 4; }
 
@@ -234,7 +235,7 @@ extern "C" prism_status_t prism_block_norm_fwd(const prism_block_norm_t* n, cons
     a.R = n->rows;
     a.rpg = n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
     a.C = C; a.norm = n->norm; a.post = n->post_norm; a.eps = n->eps; a.res = n->res_scale;
-    const int unit = unit_of(C, {a.ld_x, h ? a.ld_h : 0, h ? a.ld_z : 0, has_y ? a.ld_y : 0, gate ? a.ld_gate : 0,
+    const int unit = unit_of(es == 2 ? 8 : 4, C, {a.ld_x, h ? a.ld_h : 0, h ? a.ld_z : 0, has_y ? a.ld_y : 0, gate ? a.ld_gate : 0,
                                  scale ? a.ld_scale : 0, shift ? a.ld_shift : 0},
                              {x, h, gate, w_post, w, b, scale, shift, z, y});
     if (n->stream_dtype == PRISM_BF16) st = launch_fwd<__nv_bfloat16, __nv_bfloat16>(a, unit, stream);
@@ -290,7 +291,7 @@ extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, cons
     a.R = n->rows;
     a.rpg = s.rpg; a.groups = s.groups; a.segs = s.segs; a.per_group = s.per_group;
     a.C = C; a.norm = n->norm; a.post = n->post_norm; a.eps = n->eps; a.res = n->res_scale;
-    const int unit = unit_of(C, {has_y ? a.ld_z : 0, h ? a.ld_h : 0, dz ? a.ld_dz : 0, has_y ? a.ld_dy : 0, a.ld_dx,
+    const int unit = unit_of(es == 2 ? 8 : 4, C, {has_y ? a.ld_z : 0, h ? a.ld_h : 0, dz ? a.ld_dz : 0, has_y ? a.ld_dy : 0, a.ld_dx,
                                  h ? a.ld_dh : 0, gate ? a.ld_gate : 0, scale ? a.ld_scale : 0},
                              {has_y ? z : nullptr, h, gate, w_post, w, b, scale, dz, dy, dx, dh, dgate, dscale, dshift,
                               part ? ws : nullptr});

@@ -94,9 +94,51 @@ template <int E> __device__ __forceinline__ void store_vec(float* p, const float
     }
 }
 
-template <typename TX, typename TH, int E, int MAXT, bool HAS_H, int CTAS>
+// Rows on their way to a team's threads: through shared memory, D rows ahead (Lane), or, for elements of two bytes
+// that lie on no wider boundary, through registers, one row ahead.
+extern __shared__ __align__(16) char g_ring[];
+
+// A thread's eight channels, of the packs that hold them, in fp32.
+template <typename T, int E> __device__ __forceinline__ void unpack_units(const Pack<T, E> (&p)[8 / E], F2 (&f)[4]) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8 / E; ++u) unpack<E>(p[u], v + u * E);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(v[2 * i], v[2 * i + 1]);
+}
+template <typename T, int E> __device__ __forceinline__ void clear_units(Pack<T, E> (&p)[8 / E]) {
+#pragma unroll
+    for (int u = 0; u < 8 / E; ++u)
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(p[u].w) / 4); ++i) p[u].w[i] = 0u;
+}
+// and stored, where they are the row's
+template <typename T, int E> __device__ __forceinline__ void put_units(T* row, const F2 (&v)[4], int t, int team, int C) {
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = both(v[i]);
+        o[2 * i] = f.x;
+        o[2 * i + 1] = f.y;
+    }
+#pragma unroll
+    for (int u = 0; u < 8 / E; ++u) {
+        const int c = (u * team + t) * E;
+        if (c < C) {
+            Pack<T, E> p;
+            pack<E>(p, o + u * E);
+            store(row + c, p);
+        }
+    }
+}
+
+// D > 0: D rows ahead through shared memory (teams that have an SM to themselves), else one through registers.
+template <typename TX, typename TH, int E, int MAXT, bool HAS_H, int CTAS, int D>
 __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fwd(const FwdArgs a) {
     constexpr int U = 8 / E;
+    constexpr bool RING = D > 0;
+    using LX = Lane<TX, E>;
+    using LH = Lane<TH, E>;
     __shared__ float sums[Team<MAXT>::kFloats];
     Team<MAXT> team;
     team.init(sums);
@@ -113,141 +155,145 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fw
     const float fc = (float)C, inv_c = 1.f / fc;
     const TX* x = (const TX*)a.x;
     const TH* h = (const TH*)a.h;
+    auto in = [&](int i) { return ((i / E) * T + t) * E < C; };          // whether channel i of the thread's eight is the row's
+    auto pair = [&](float m, int i) { return f2(in(2 * i) ? m : 0.f, in(2 * i + 1) ? m : 0.f); };
 
-    Pack<TX, E> rx[U];
-    Pack<TH, E> rh[U];
-    auto fetch = [&](int64_t r) {
+    const uint32_t ring = RING ? (uint32_t)__cvta_generic_to_shared(g_ring) : 0u;
+    const int o_h = LX::kBytes * T, stage_bytes = o_h + (HAS_H ? LH::kBytes * T : 0);
+    Pack<TX, E> rx[RING ? 1 : U];
+    Pack<TH, E> rh[RING ? 1 : U];
+    if constexpr (RING) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = (u * T + t) * E;
-            if (c < C) {
-                load(rx[u], x + r * a.ld_x + c);
-                if (HAS_H) load(rh[u], h + r * a.ld_h + c);
+        for (int i = 0; i < D; ++i) {
+            LX::clear(g_ring + i * stage_bytes, T, t, t, T, C, false);
+            if constexpr (HAS_H) LH::clear(g_ring + i * stage_bytes + o_h, T, t, t, T, C, false);
+        }
+    } else {
+        clear_units<TX, E>(rx);
+        clear_units<TH, E>(rh);
+    }
+    auto fetch = [&](int64_t r, int stage) {
+        if constexpr (RING) {
+            if (r < r1) {
+                LX::fetch(ring + stage * stage_bytes, T, t, x + r * a.ld_x, t, T, C);
+                if constexpr (HAS_H) LH::fetch(ring + stage * stage_bytes + o_h, T, t, h + r * a.ld_h, t, T, C);
+            }
+            cp_commit();
+        } else if (r < r1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (u * T + t) * E;
+                if (c < C) {
+                    load(rx[u], x + r * a.ld_x + c);
+                    if (HAS_H) load(rh[u], h + r * a.ld_h + c);
+                }
             }
         }
     };
-    fetch(r0);
+#pragma unroll
+    for (int i = 0; i < (RING ? D : 1); ++i) fetch(r0 + i * step, i);
 
-    float mul[U * E], add[U * E], gate[HAS_H ? U * E : 1];
+    F2 mul[4], add[4], gate[HAS_H ? 4 : 1];
     auto vectors = [&](int64_t g) {
+        float m[8], n[8], q[HAS_H ? 8 : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = (u * T + t) * E;
             float s[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) { mul[u * E + e] = 1.f; add[u * E + e] = 0.f; }
+            for (int e = 0; e < E; ++e) { m[u * E + e] = 1.f; n[u * E + e] = 0.f; }
             if constexpr (HAS_H) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) gate[u * E + e] = 1.f;
+                for (int e = 0; e < E; ++e) q[u * E + e] = 1.f;
             }
             if (c >= C) continue;
             if (a.norm != PRISM_NORM_NONE) {
-                if (a.w) load_vec<E>(mul + u * E, a.w + c);
-                if (a.b) load_vec<E>(add + u * E, a.b + c);
+                if (a.w) load_vec<E>(m + u * E, a.w + c);
+                if (a.b) load_vec<E>(n + u * E, a.b + c);
                 if (a.scale) {
                     load_vec<E>(s, a.scale + g * a.ld_scale + c);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) { mul[u * E + e] *= 1.f + s[e]; add[u * E + e] *= 1.f + s[e]; }
+                    for (int e = 0; e < E; ++e) { m[u * E + e] *= 1.f + s[e]; n[u * E + e] *= 1.f + s[e]; }
                 }
                 if (a.shift) {
                     load_vec<E>(s, a.shift + g * a.ld_shift + c);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) add[u * E + e] += s[e];
+                    for (int e = 0; e < E; ++e) n[u * E + e] += s[e];
                 }
             }
             if constexpr (HAS_H) {
-                if (a.gate) load_vec<E>(gate + u * E, a.gate + g * a.ld_gate + c);
+                if (a.gate) load_vec<E>(q + u * E, a.gate + g * a.ld_gate + c);
                 if (a.w_post) {
                     load_vec<E>(s, a.w_post + c);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) gate[u * E + e] *= s[e];
+                    for (int e = 0; e < E; ++e) q[u * E + e] *= s[e];
                 }
             }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mul[i] = f2(m[2 * i], m[2 * i + 1]);
+            add[i] = f2(n[2 * i], n[2 * i + 1]);
+            if constexpr (HAS_H) gate[i] = f2(in(2 * i) ? q[2 * i] : 0.f, in(2 * i + 1) ? q[2 * i + 1] : 0.f);
         }
     };
     int64_t g = r0 / a.rpg, next = (g + 1) * a.rpg;
     vectors(g);
 
+    int stage = 0;
     for (int64_t r = r0; r < r1; r += step) {
-        float v[U * E];
-#pragma unroll
-        for (int i = 0; i < U * E; ++i) v[i] = 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if ((u * T + t) * E < C) unpack<E>(rx[u], v + u * E);
-        float hv[HAS_H ? U * E : 1];
-        if constexpr (HAS_H) {
-#pragma unroll
-            for (int i = 0; i < U * E; ++i) hv[i] = 0.f;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((u * T + t) * E < C) unpack<E>(rh[u], hv + u * E);
+        F2 v[4], hv[HAS_H ? 4 : 1];
+        if constexpr (RING) {
+            cp_wait<D - 1>();
+            LX::read(v, g_ring + stage * stage_bytes, T, t);
+            if constexpr (HAS_H) LH::read(hv, g_ring + stage * stage_bytes + o_h, T, t);
+        } else {
+            unpack_units<TX, E>(rx, v);
+            if constexpr (HAS_H) unpack_units<TH, E>(rh, hv);
+            fetch(r + step, 0);
         }
-        if (r + step < r1) fetch(r + step);
         if (r >= next) {                  // steps are shorter than groups
             vectors(++g);
             next += a.rpg;
         }
 
-        // mean (layer) and 1/std of the row held in f; f becomes f - mean
-        auto stats = [&](float* f, int kind) {
+        // 1/std of the row held in f; f becomes f - mean (layer)
+        auto stats = [&](F2 (&f)[4], int kind) {
             if (kind == PRISM_NORM_LAYER) {
-                float s = 0.f;
+                const float m = -mean_of(team.sum1(sum((f[0] + f[1]) + (f[2] + f[3]))), fc, inv_c);
 #pragma unroll
-                for (int i = 0; i < U * E; ++i) s += f[i];
-                const float m = mean_of(team.sum1(s), fc, inv_c);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if ((u * T + t) * E < C) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e) f[u * E + e] -= m;
-                    }
+                for (int i = 0; i < 4; ++i) f[i] = f[i] + pair(m, i);
             }
-            float q = 0.f;
+            F2 q = f[0] * f[0];
 #pragma unroll
-            for (int i = 0; i < U * E; ++i) q = fmaf(f[i], f[i], q);
-            return rsqrtf(team.sum1(q) * inv_c + a.eps);
+            for (int i = 1; i < 4; ++i) q = fma(f[i], f[i], q);
+            return rsqrtf(team.sum1(sum(q)) * inv_c + a.eps);
         };
 
         if constexpr (HAS_H) {
             if (a.post != PRISM_NORM_NONE) {
-                const float rh_ = stats(hv, a.post);
+                const F2 rh_ = f2(stats(hv, a.post));
 #pragma unroll
-                for (int i = 0; i < U * E; ++i) hv[i] *= rh_;
+                for (int i = 0; i < 4; ++i) hv[i] = hv[i] * rh_;
             }
+            const F2 res = f2(a.res);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = (u * T + t) * E;
-                if (c < C) {
-#pragma unroll
-                    for (int i = u * E; i < u * E + E; ++i) v[i] = fmaf(a.res, v[i], gate[i] * hv[i]);
-                    Pack<TX, E> o;
-                    pack<E>(o, v + u * E);
-                    store((TX*)a.z + r * a.ld_z + c, o);
-                }
-            }
+            for (int i = 0; i < 4; ++i) v[i] = fma(res, v[i], gate[i] * hv[i]);
+            put_units<TX, E>((TX*)a.z + r * a.ld_z, v, t, T, C);
         }
         if (a.norm != PRISM_NORM_NONE) {
-            const float rs = stats(v, a.norm);
+            const F2 rs = f2(stats(v, a.norm));
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = (u * T + t) * E;
-                if (c < C) {
-                    float o[E];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] = fmaf(v[u * E + e] * rs, mul[u * E + e], add[u * E + e]);
-                    Pack<TH, E> p;
-                    pack<E>(p, o);
-                    store((TH*)a.y + r * a.ld_y + c, p);
-                }
-            }
+            for (int i = 0; i < 4; ++i) v[i] = fma(v[i] * rs, mul[i], add[i]);
+            put_units<TH, E>((TH*)a.y + r * a.ld_y, v, t, T, C);
+        }
+        if constexpr (RING) {             // the row's own values have been used: their place is free
+            fetch(r + D * step, stage);
+            stage = stage + 1 == D ? 0 : stage + 1;
         }
     }
+    if constexpr (RING) cp_wait<0>();
 }
-
-// Rows on their way to a team's threads: through shared memory, D rows ahead (Lane), or, for elements of two bytes
-// that lie on no wider boundary, through registers, one row ahead.
-extern __shared__ __align__(16) char g_ring[];
 
 constexpr bool vec_shared(int maxt) { return maxt > 640; }
 
@@ -306,8 +352,10 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
             if constexpr (HAS_H) LH::clear(s + o_h, threads, tid, t, T, C, false);
         }
     } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) rz[u].w[0] = rdz[u].w[0] = rh[u].w[0] = rdy[u].w[0] = 0u;   // E = 1
+        clear_units<TX, E>(rz);
+        clear_units<TX, E>(rdz);
+        clear_units<TH, E>(rdy);
+        clear_units<TH, E>(rh);
     }
     auto fetch = [&](int64_t r, int stage) {
         if constexpr (RING) {
@@ -419,20 +467,10 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
                 LX::read(d, s + o_dz, threads, tid);
                 if constexpr (HAS_H) LH::read(h, s + o_h, threads, tid);
             } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f[2];
-                    unpack<1>(rz[2 * i], f); unpack<1>(rz[2 * i + 1], f + 1);
-                    z[i] = f2(f[0], f[1]);
-                    unpack<1>(rdy[2 * i], f); unpack<1>(rdy[2 * i + 1], f + 1);
-                    dy[i] = f2(f[0], f[1]);
-                    unpack<1>(rdz[2 * i], f); unpack<1>(rdz[2 * i + 1], f + 1);
-                    d[i] = f2(f[0], f[1]);
-                    if constexpr (HAS_H) {
-                        unpack<1>(rh[2 * i], f); unpack<1>(rh[2 * i + 1], f + 1);
-                        h[i] = f2(f[0], f[1]);
-                    }
-                }
+                unpack_units<TX, E>(rz, z);
+                unpack_units<TH, E>(rdy, dy);
+                unpack_units<TX, E>(rdz, d);
+                if constexpr (HAS_H) unpack_units<TH, E>(rh, h);
                 fetch(r + step, 0);
             }
 
@@ -497,31 +535,12 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
                     }
                 }
             }
-            auto put = [&](auto* row, const F2 (&v)[4]) {
-                using TO = typename std::remove_reference<decltype(*row)>::type;
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = both(v[i]);
-                    o[2 * i] = f.x;
-                    o[2 * i + 1] = f.y;
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int c = (u * T + t) * E;
-                    if (c < C) {
-                        Pack<TO, E> p;
-                        pack<E>(p, o + u * E);
-                        store(row + c, p);
-                    }
-                }
-            };
             {
                 F2 o[4];
                 const F2 res = f2(HAS_H ? a.res : 1.f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[i] = HAS_H ? d[i] * res : d[i];
-                put((TX*)a.dx + r * a.ld_dx, o);
+                put_units<TX, E>((TX*)a.dx + r * a.ld_dx, o, t, T, C);
             }
             if constexpr (HAS_H) {
                 F2 q[2], gate[4];
@@ -543,7 +562,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
 #pragma unroll
                     for (int i = 0; i < 4; ++i) d[i] = rr * fma(h[i], mdn, d[i] + md);
                 }
-                put((TH*)a.dh + r * a.ld_dh, d);
+                put_units<TH, E>((TH*)a.dh + r * a.ld_dh, d, t, T, C);
             }
             if constexpr (RING) {             // the row's own values have been used: their place is free
                 fetch(r + D * step, stage);
@@ -624,6 +643,8 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
     let_next_start();
 }
 
+// channels of the widest access: 16 bytes of the stream, so that a warp's access leaves no gaps
+template <typename TX> constexpr int wide_unit() { return 16 / (int)sizeof(TX); }
 // threads of a team: 8 channels a thread; 8, 16 or a whole number of warps
 inline int team_threads(int C) {
     const int n = (C + 7) / 8;
@@ -638,7 +659,7 @@ inline int cta_teams(int C) {
 constexpr int team_bucket(int threads) {
     return threads <= 32 ? 32 : threads <= 256 ? 256 : threads <= 384 ? 384 : threads <= 512 ? 512 : threads <= 640 ? 640 : threads <= 768 ? 768 : 1024;
 }
-constexpr int fwd_ctas(int maxt) { return maxt <= 256 ? 3 : maxt <= 384 ? 2 : 1; }
+constexpr int fwd_ctas(int maxt, int unit) { return maxt == 32 ? 2 : maxt <= 256 ? (unit >= 4 ? 3 : 2) : maxt <= 384 ? 2 : 1; }
 constexpr int bwd_ctas(int maxt) { return maxt <= 256 ? 2 : 1; }
 // teams that run at a time on an SM
 inline int sm_teams(int C, int ctas) {
@@ -664,7 +685,14 @@ prism_status_t launch_bwd_one(const BwdArgs& a, dim3 grid, dim3 block, cudaStrea
 }
 template <typename TX, typename TH, int E, int MAXT, int H>
 prism_status_t launch_fwd_one(const FwdArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
-    k_block_norm_fwd<TX, TH, E, MAXT, H != kNoBranch, fwd_ctas(MAXT)><<<grid, block, 0, s>>>(a);
+    constexpr bool async = Lane<TX, E>::kAsync && Lane<TH, E>::kAsync && MAXT > 256;
+    constexpr int row = 8 * (int)(sizeof(TX) + (H != kNoBranch ? sizeof(TH) : 0)), ctas = fwd_ctas(MAXT, E);
+    constexpr int most = (216 << 10) / ctas / (row * MAXT), D = !async ? 0 : most > kRowsAhead ? kRowsAhead : most;
+    auto kernel = &k_block_norm_fwd<TX, TH, E, MAXT, H != kNoBranch, ctas, D>;
+    const int bytes = D * row * (int)block.x;
+    if (bytes > 40 << 10 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return PRISM_ERR_CUDA;
+    kernel<<<grid, block, bytes, s>>>(a);
     return PRISM_OK;
 }
 
@@ -685,7 +713,8 @@ template <typename TX, typename TH> prism_status_t launch_bwd(const BwdArgs& a, 
 
 #define PRISM_BN_BY_UNIT(ONE, TX, TH, H)                                              \
     do {                                                                              \
-        if (unit == 8) PRISM_BN_BY_SIZE(ONE, TX, TH, 8, H)                            \
+        constexpr int kWide = wide_unit<TX>();                                        \
+        if (unit == kWide) PRISM_BN_BY_SIZE(ONE, TX, TH, kWide, H)                    \
         if (unit == 2) PRISM_BN_BY_SIZE(ONE, TX, TH, 2, H)                            \
         PRISM_BN_BY_SIZE(ONE, TX, TH, 1, H)                                           \
     } while (0)
@@ -694,7 +723,7 @@ template <typename TX, typename TH> prism_status_t launch_bwd(const BwdArgs& a, 
     template <> prism_status_t launch_fwd<TX, TH>(const FwdArgs& a, int unit, cudaStream_t s) {        \
         const dim3 block(team_threads(a.C), cta_teams(a.C));                                           \
         const int64_t want = (a.R + block.y - 1) / block.y;                                            \
-        const int64_t most = kSMs * (int64_t)sm_teams(a.C, fwd_ctas(team_bucket(block.x))) / block.y;  \
+        const int64_t most = kSMs * (int64_t)sm_teams(a.C, fwd_ctas(team_bucket(block.x), unit)) / block.y;  \
         const dim3 grid((unsigned)(want < most ? want : most));                                        \
         if (a.h) PRISM_BN_BY_UNIT(launch_fwd_one, TX, TH, kPlain);                                     \
         else PRISM_BN_BY_UNIT(launch_fwd_one, TX, TH, kNoBranch);                                      \

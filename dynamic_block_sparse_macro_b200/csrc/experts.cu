@@ -197,15 +197,14 @@ __global__ void __launch_bounds__(1024, 2) k_expert_place(const PlanArgs a) {
             }
         }
     }
-    // rows without a slot: behind each expert's last one, and behind the last expert
-    const int64_t me = (int64_t)blockIdx.x * 1024 + tid, all = (int64_t)gridDim.x * 1024;
+    // rows without a slot: behind each expert's last one (a warp an expert), and behind the last expert
     if (a.align > 1)
-        for (int64_t i = me; i < (int64_t)E * (a.align - 1); i += all) {
-            const int e = (int)(i / (a.align - 1)), row = before[e] + total[e] + (int)(i % (a.align - 1));
+        for (int e = (int)blockIdx.x * 32 + (tid >> 5); e < E; e += (int)gridDim.x * 32) {
             const int next = e + 1 < E ? before[e + 1] : whole;
-            if (row < next) a.src[row] = -1;
+            for (int row = before[e] + total[e] + lane; row < next; row += 32) a.src[row] = -1;
         }
-    for (int64_t row = whole + me; row < a.cap; row += all) a.src[row] = -1;
+    for (int64_t row = whole + (int64_t)blockIdx.x * 1024 + tid; row < a.cap; row += (int64_t)gridDim.x * 1024)
+        a.src[row] = -1;
 }
 
 // ------------------------------------------------------------------ moves
@@ -226,21 +225,23 @@ struct MoveArgs {
 constexpr int kTailCtas = kSMs;
 template <typename T, int N> __device__ __forceinline__ void clear_rows(const MoveArgs& a, T* sorted) {
     const int i = (int)(blockIdx.x - a.token_ctas);
-    int64_t r0, r1, step = 1;
+    int64_t r0, r1;
     if (i < a.gap_ctas) {
         r0 = (int64_t)a.offsets[i] + a.counts[i];
         r1 = a.offsets[i + 1];
     } else {
-        r0 = (int64_t)a.offsets[a.E] + (i - a.gap_ctas);
-        r1 = a.cap;
-        step = kTailCtas;
+        const int64_t used = a.offsets[a.E], left = a.cap - used;
+        r0 = used + left * (i - a.gap_ctas) / kTailCtas;
+        r1 = used + left * (i - a.gap_ctas + 1) / kTailCtas;
     }
     if (r0 < 0 || r1 > a.cap) return;
     Pack<T, N> z;
 #pragma unroll
     for (int j = 0; j < (int)(sizeof(z.w) / 4); ++j) z.w[j] = 0u;
-    for (int64_t r = r0; r < r1; r += step)
-        for (int u = threadIdx.x; u < a.units; u += blockDim.x) store(sorted + r * a.C + (int64_t)u * N, z);
+    // rows are dense: one run of accesses
+    T* p = sorted + r0 * a.C;
+    const int64_t n = (r1 - r0) * a.units;
+    for (int64_t u = threadIdx.x; u < n; u += blockDim.x) store(p + u * N, z);
 }
 
 // this token's rows: lane j holds pos of choice j, -1 where there is none
@@ -586,12 +587,17 @@ extern "C" prism_status_t prism_expert_combine(const prism_experts_t* e, int32_t
     a.y = y; a.w = weights; a.add = add; a.out = out;
     const int b = unit_bytes(esz, channels, {a.ld_out, add ? a.ld_add : 0}, {y, add, out});
     a.units = (int)(channels * esz / b);
-    const int J = a.k <= 1 ? 1 : a.k <= 2 ? 2 : 4, lanes = 32 * (8 / J);
+    // choices at a time: up to four, or eight of short rows, whose lanes' further accesses would be idle
+    int J = a.k <= 1 ? 1 : a.k <= 2 ? 2 : 4;
+    if (a.units <= 32 && a.k > 4) J = 8;
+    const int lanes = 32 * (8 / J);
     a.segs = (a.units + lanes - 1) / lanes;
     unsigned grid;
     if (!grid_of((a.R * a.segs + 7) / 8, false, 1, 0, &a, &grid)) return PRISM_ERR_UNSUPPORTED;
     if (J == 1) launch_combine<1, true>(dtype, b, grid, stream, a);
     else if (J == 2) launch_combine<2, true>(dtype, b, grid, stream, a);
+    else if (J == 8 && a.k <= 8) launch_combine<8, true>(dtype, b, grid, stream, a);
+    else if (J == 8) launch_combine<8, false>(dtype, b, grid, stream, a);
     else if (a.k <= 4) launch_combine<4, true>(dtype, b, grid, stream, a);
     else launch_combine<4, false>(dtype, b, grid, stream, a);
     return launch_status(1);
