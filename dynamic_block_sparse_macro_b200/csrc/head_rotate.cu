@@ -137,16 +137,46 @@ __device__ __forceinline__ void angles(const Args& a, uint32_t token, int l, F2 
     }
 }
 
-// CTAs on an SM and heads of a lane on their way at a time: what the registers allow without spills, at 24 heads of 128
-// channels.  Forward: bf16 5 x 2 1150 us, 3 x 4 1182, 4 x 4 1206 (294912 tokens); f32 3 x 4 251-271, 5 x 2 266-295
-// (30720).  Backward: bf16 3 x 2 401 us, 2 x 2 485, 4 x 1 466 (61440 tokens); f32 2 x 2 355, 3 x 2 437 (30720).
+// A lane's channels of one head on their way through its own part of shared memory, in planes of one access a thread.
+template <typename T, bool HALF> struct Copy {
+    static constexpr int B = HALF ? 4 * (int)sizeof(T) : 16, P = 8 * (int)sizeof(T) / B;
+    template <int D> static __device__ __forceinline__ void fetch(uint32_t s, const T* head) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) cp_async<B>(s + p * 256 * B, head + p * (HALF ? D / 2 : 16 / (int)sizeof(T)));
+    }
+    static __device__ __forceinline__ void read(Raw<T, HALF>& r, const char* s) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(s + p * 256 * B);
+            uint32_t* w = HALF ? r.p[p * HALF].w : r.p[0].w + 4 * p;
+            if constexpr (B == 16) {
+                const uint4 v = *reinterpret_cast<const uint4*>(q);
+                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(q);
+                w[0] = v.x; w[1] = v.y;
+            }
+        }
+    }
+};
+
+// CTAs on an SM, heads of a lane at a time and steps that are copied ahead (0: a step's rows are loaded when it begins):
+// what the registers allow without spills, at 24 heads of 128 channels.
+// Forward: bf16 5 x 2 1150 us, 3 x 4 1182, 4 x 4 1206 (294912 tokens); f32 3 x 4 251-271, 5 x 2 266-295 (30720).
+// Backward (61440 tokens, bf16): interleaved 3 x 1, 4 ahead 364 us, 3 x 2, 2 ahead 402, without copies 401; half
+// 3 x 2, 2 ahead 358, 3 x 1, 4 ahead 380.  f32 (30720): 2 x 2 without copies 355; a lane's eight floats are two
+// copies that leave gaps in a warp's access: interleaved 585.
 constexpr int ctas_sm(int elem, bool bwd) { return bwd ? (elem == 2 ? 3 : 2) : elem == 2 ? 5 : 3; }
-constexpr int heads_at_once(int elem, bool bwd) { return bwd || elem == 2 ? 2 : 4; }
+constexpr int heads_at_once(int elem, bool half, bool bwd) { return bwd ? (elem == 2 && !half ? 1 : 2) : elem == 2 ? 2 : 4; }
+constexpr int steps_ahead(int elem, bool half, bool bwd) { return bwd && elem == 2 ? (half ? 2 : 4) : 0; }
+extern __shared__ __align__(16) char g_rows[];
 
 template <typename T, int D, bool HALF, bool BWD>
 __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(const Args a) {
     constexpr int LPH = D / 8, TPW = 32 / LPH;       // lanes a head, heads a warp
-    constexpr int HU = heads_at_once(sizeof(T), BWD);
+    constexpr int HU = heads_at_once(sizeof(T), HALF, BWD), S = steps_ahead(sizeof(T), HALF, BWD);
+    using CP = Copy<T, HALF>;
+    constexpr int kRow = CP::P * CP::B * 256, kStage = 2 * HU * kRow;     // of a CTA: one head a lane, x and dr of a step
     const Side& sd = a.side[blockIdx.y];
     const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH;
     // the same for all lanes, and so known to the compiler: its step's counters and rows need no registers of theirs
@@ -164,88 +194,138 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
             w.b[i] = f2(__ldg(sd.w + channel<D, HALF>(l, 2 * i, true)), __ldg(sd.w + channel<D, HALF>(l, 2 * i + 1, true)));
         }
     }
-    for (int64_t it = (int64_t)blockIdx.x * 8 + warp; it < items; it += warps) {
-        const uint32_t token = sd.parts == 1 ? (uint32_t)it : (uint32_t)(it / sd.parts);
-        const int first = (int)(it - (int64_t)token * sd.parts) * TPW;
-        const T* x = (const T*)sd.x + (int64_t)token * sd.ld_x + c0;
-        const T* dr = BWD ? (const T*)sd.dr + (int64_t)token * sd.ld_dr + c0 : nullptr;
-        T* out = (T*)sd.out + (int64_t)token * sd.ld_out + c0;
-        F2 cs[2], sn[2], sm[2];                      // sm = -sn
-        // Every lane of the warp takes part in the exchanges of every step.  Lanes past the last head repeat it; they
-        // neither store nor add to dw.
-        for (int h0 = first; h0 < sd.heads; h0 += HU * stride) {
-            Raw<T, HALF> px[HU], pr[BWD ? HU : 1];
-            bool in[HU];
+    // A step: HU heads of each of the warp's lane groups, of one token.
+    struct Step {
+        int64_t it;
+        uint32_t token;
+        int first, h0;
+    };
+    auto begin = [&](Step& s, int64_t it) {
+        s.it = it;
+        s.token = sd.parts == 1 ? (uint32_t)it : (uint32_t)(it / sd.parts);
+        s.first = s.h0 = (int)(it - (int64_t)s.token * sd.parts) * TPW;
+    };
+    auto advance = [&](Step& s) {
+        s.h0 += HU * stride;
+        if (s.h0 >= sd.heads) begin(s, s.it + warps);
+    };
+    // lanes past the last head repeat it; they neither store nor add to dw
+    auto head_of = [&](const Step& s, int u) {
+        const int h = s.h0 + sub + u * stride;
+        return h < sd.heads ? h : sd.heads - 1;
+    };
+    Step now, ahead;
+    begin(now, (int64_t)blockIdx.x * 8 + warp);
+    ahead = now;
+    const uint32_t ring = S ? (uint32_t)__cvta_generic_to_shared(g_rows) + threadIdx.x * CP::B : 0u;
+    int stage = 0;
+    auto fetch = [&](int st) {
+        if (ahead.it < items) {
+            const T* x = (const T*)sd.x + (int64_t)ahead.token * sd.ld_x + c0;
+            const T* dr = (const T*)sd.dr + (int64_t)ahead.token * sd.ld_dr + c0;
 #pragma unroll
             for (int u = 0; u < HU; ++u) {
-                int h = h0 + sub + u * stride;
-                in[u] = h < sd.heads;
-                h = in[u] ? h : sd.heads - 1;
-                if (!BWD || a.norm) load_raw<T, D, HALF>(px[u], x + h * D);
-                if constexpr (BWD) load_raw<T, D, HALF>(pr[u], dr + h * D);
+                const int h = head_of(ahead, u) * D;
+                if (a.norm) CP::template fetch<D>(ring + st * kStage + 2 * u * kRow, x + h);
+                CP::template fetch<D>(ring + st * kStage + (2 * u + 1) * kRow, dr + h);
             }
-            if (h0 == first) {
-                angles(a, token, l, cs, sn);
-                sm[0] = sn[0] * f2(-1.f);
-                sm[1] = sn[1] * f2(-1.f);
-            }
+            advance(ahead);
+        }
+        cp_commit();
+    };
+    if constexpr (S > 0) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) fetch(i);
+    }
+    F2 cs[2], sn[2], sm[2];                      // sm = -sn
+    // every lane of the warp takes part in the exchanges of every step
+    while (now.it < items) {
+        Raw<T, HALF> px[HU], pr[BWD ? HU : 1];
+        if constexpr (S > 0) {
+            cp_wait<S - 1>();
+        } else {
+            const T* x = (const T*)sd.x + (int64_t)now.token * sd.ld_x + c0;
+            const T* dr = (const T*)sd.dr + (int64_t)now.token * sd.ld_dr + c0;
 #pragma unroll
             for (int u = 0; u < HU; ++u) {
-                Pairs v, o;
-                if (!BWD || a.norm) v = pairs_of<T, HALF>(px[u]);
-                if constexpr (!BWD) {
-                    if (a.norm) {
-                        const float q = lanes_sum<LPH>(sum(fma(v.a[0], v.a[0], v.a[1] * v.a[1]) +
-                                                           fma(v.b[0], v.b[0], v.b[1] * v.b[1])));
-                        const F2 r = f2(rsqrtf(q * (1.f / D) + a.eps));
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            v.a[i] = v.a[i] * (r * w.a[i]);
-                            v.b[i] = v.b[i] * (r * w.b[i]);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        o.a[i] = fma(v.a[i], cs[i], v.b[i] * sm[i]);
-                        o.b[i] = fma(v.a[i], sn[i], v.b[i] * cs[i]);
-                    }
-                } else {
-                    const Pairs d = pairs_of<T, HALF>(pr[u]);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        o.a[i] = fma(d.a[i], cs[i], d.b[i] * sn[i]);
-                        o.b[i] = fma(d.b[i], cs[i], d.a[i] * sm[i]);
-                    }
-                    if (a.norm) {
-                        // x once against itself, once against dn ∘ w; dx = r dn ∘ w - x r³ mean(dn ∘ w ∘ x)
-                        Pairs t;
-                        F2 q2 = v.a[0] * v.a[0], m2;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            t.a[i] = o.a[i] * v.a[i];
-                            t.b[i] = o.b[i] * v.b[i];
-                            if (i) q2 = fma(v.a[i], v.a[i], q2);
-                            q2 = fma(v.b[i], v.b[i], q2);
-                            m2 = i ? fma(t.a[i], w.a[i], m2) : t.a[i] * w.a[i];
-                            m2 = fma(t.b[i], w.b[i], m2);
-                        }
-                        float q = sum(q2), m = sum(m2);
-                        lanes_sum<LPH>(q, m, l);
-                        const float r = rsqrtf(q * (1.f / D) + a.eps);
-                        const F2 r2 = f2(r), rd = f2(in[u] ? r : 0.f), k = f2(-(r * r) * (r * m) * (1.f / D));
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            dw.a[i] = fma(t.a[i], rd, dw.a[i]);
-                            dw.b[i] = fma(t.b[i], rd, dw.b[i]);
-                            o.a[i] = fma(v.a[i], k, o.a[i] * w.a[i] * r2);
-                            o.b[i] = fma(v.b[i], k, o.b[i] * w.b[i] * r2);
-                        }
-                    }
-                }
-                if (in[u]) store_pairs<T, D, HALF>(out + (h0 + sub + u * stride) * D, o);
+                const int h = head_of(now, u) * D;
+                if (!BWD || a.norm) load_raw<T, D, HALF>(px[u], x + h);
+                if constexpr (BWD) load_raw<T, D, HALF>(pr[u], dr + h);
             }
         }
+        if (now.h0 == now.first) {
+            angles(a, now.token, l, cs, sn);
+            sm[0] = sn[0] * f2(-1.f);
+            sm[1] = sn[1] * f2(-1.f);
+        }
+        T* out = (T*)sd.out + (int64_t)now.token * sd.ld_out + c0;
+#pragma unroll
+        for (int u = 0; u < HU; ++u) {
+            const bool in = now.h0 + sub + u * stride < sd.heads;
+            Pairs v, o;
+            if constexpr (!BWD) {
+                v = pairs_of<T, HALF>(px[u]);
+                if (a.norm) {
+                    const float q = lanes_sum<LPH>(sum(fma(v.a[0], v.a[0], v.a[1] * v.a[1]) +
+                                                       fma(v.b[0], v.b[0], v.b[1] * v.b[1])));
+                    const F2 r = f2(rsqrtf(q * (1.f / D) + a.eps));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        v.a[i] = v.a[i] * (r * w.a[i]);
+                        v.b[i] = v.b[i] * (r * w.b[i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    o.a[i] = fma(v.a[i], cs[i], v.b[i] * sm[i]);
+                    o.b[i] = fma(v.a[i], sn[i], v.b[i] * cs[i]);
+                }
+            } else {
+                const char* row = g_rows + stage * kStage + 2 * u * kRow + threadIdx.x * CP::B;
+                if constexpr (S > 0) CP::read(pr[u], row + kRow);
+                const Pairs d = pairs_of<T, HALF>(pr[u]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    o.a[i] = fma(d.a[i], cs[i], d.b[i] * sn[i]);
+                    o.b[i] = fma(d.b[i], cs[i], d.a[i] * sm[i]);
+                }
+                if (a.norm) {
+                    if constexpr (S > 0) CP::read(px[u], row);
+                    v = pairs_of<T, HALF>(px[u]);
+                    // x once against itself, once against dn ∘ w; dx = r dn ∘ w - x r³ mean(dn ∘ w ∘ x)
+                    Pairs t;
+                    F2 q2 = v.a[0] * v.a[0], m2;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        t.a[i] = o.a[i] * v.a[i];
+                        t.b[i] = o.b[i] * v.b[i];
+                        if (i) q2 = fma(v.a[i], v.a[i], q2);
+                        q2 = fma(v.b[i], v.b[i], q2);
+                        m2 = i ? fma(t.a[i], w.a[i], m2) : t.a[i] * w.a[i];
+                        m2 = fma(t.b[i], w.b[i], m2);
+                    }
+                    float q = sum(q2), m = sum(m2);
+                    lanes_sum<LPH>(q, m, l);
+                    const float r = rsqrtf(q * (1.f / D) + a.eps);
+                    const F2 r2 = f2(r), rd = f2(in ? r : 0.f), k = f2(-(r * r) * (r * m) * (1.f / D));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        dw.a[i] = fma(t.a[i], rd, dw.a[i]);
+                        dw.b[i] = fma(t.b[i], rd, dw.b[i]);
+                        o.a[i] = fma(v.a[i], k, o.a[i] * w.a[i] * r2);
+                        o.b[i] = fma(v.b[i], k, o.b[i] * w.b[i] * r2);
+                    }
+                }
+            }
+            if (in) store_pairs<T, D, HALF>(out + (now.h0 + sub + u * stride) * D, o);
+        }
+        advance(now);
+        if constexpr (S > 0) {                // the step's own rows have been used: their place is free
+            fetch(stage);
+            stage = stage + 1 == S ? 0 : stage + 1;
+        }
     }
+    if constexpr (S > 0) cp_wait<0>();
     if constexpr (BWD) {
         let_next_start();
         if (!a.part) return;
@@ -330,17 +410,27 @@ static unsigned ctas_of(const Args& a, int sides, int per_sm) {
     return (unsigned)(want < most ? want : most);
 }
 
-template <bool BWD> static void launch(const prism_rotate_t* p, const Args& a, dim3 grid, cudaStream_t s) {
-#define PRISM_ROT(T, D, HALF) k_head_rotate<T, D, HALF, BWD><<<grid, 256, 0, s>>>(a)
-#define PRISM_ROT_D(T)                                                                              \
-    do {                                                                                            \
-        if (p->head_dim == 128) { if (p->pairing == PRISM_PAIRS_HALF) PRISM_ROT(T, 128, true); else PRISM_ROT(T, 128, false); } \
-        else { if (p->pairing == PRISM_PAIRS_HALF) PRISM_ROT(T, 64, true); else PRISM_ROT(T, 64, false); } \
+template <typename T, int D, bool HALF, bool BWD> static prism_status_t launch_one(const Args& a, dim3 grid, cudaStream_t s) {
+    auto kernel = &k_head_rotate<T, D, HALF, BWD>;
+    constexpr int bytes = steps_ahead(sizeof(T), HALF, BWD) * 2 * heads_at_once(sizeof(T), HALF, BWD) * 8 * (int)sizeof(T) * 256;
+    if (bytes > 32 << 10 &&                       // with the static part, more than the 48 KB that need no leave
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return PRISM_ERR_CUDA;
+    kernel<<<grid, 256, bytes, s>>>(a);
+    return PRISM_OK;
+}
+template <bool BWD> static prism_status_t launch(const prism_rotate_t* p, const Args& a, dim3 grid, cudaStream_t s) {
+#define PRISM_ROT_D(T)                                                                                                 \
+    do {                                                                                                               \
+        if (p->head_dim == 128)                                                                                        \
+            return p->pairing == PRISM_PAIRS_HALF ? launch_one<T, 128, true, BWD>(a, grid, s)                          \
+                                                  : launch_one<T, 128, false, BWD>(a, grid, s);                        \
+        return p->pairing == PRISM_PAIRS_HALF ? launch_one<T, 64, true, BWD>(a, grid, s)                               \
+                                              : launch_one<T, 64, false, BWD>(a, grid, s);                             \
     } while (0)
     if (p->dtype == PRISM_BF16) PRISM_ROT_D(__nv_bfloat16);
-    else PRISM_ROT_D(float);
+    PRISM_ROT_D(float);
 #undef PRISM_ROT_D
-#undef PRISM_ROT
 }
 
 }  // namespace rot
@@ -396,15 +486,16 @@ static prism_status_t rotate(const prism_rotate_t* p, const void* Q, const void*
     const unsigned ctas = ctas_of(a, sides, ctas_sm(p->dtype == PRISM_BF16 ? 2 : 4, bwd));
     const dim3 grid(ctas, sides);
     if (!bwd) {
-        launch<false>(p, a, grid, stream);
-        return launch_status(1);
+        const prism_status_t r = launch<false>(p, a, grid, stream);
+        return r == PRISM_OK ? launch_status(1) : r;
     }
     const bool dw = dwq || dwk;
     if (dw) {
         if (!ws || ws_bytes < (size_t)kMaxCtas * p->head_dim * sizeof(float)) return PRISM_ERR_WORKSPACE;
         a.part = (float*)ws;
     }
-    launch<true>(p, a, grid, stream);
+    const prism_status_t r = launch<true>(p, a, grid, stream);
+    if (r != PRISM_OK) return r;
     if (dw) {
         if (!launch_after(k_head_rotate_join, dim3(p->head_dim / 32, sides), dim3(32, 16), 1, stream, (const float*)a.part,
                           (int)ctas, (int)p->head_dim, hq ? dwq : dwk, hq ? dwk : (float*)nullptr))

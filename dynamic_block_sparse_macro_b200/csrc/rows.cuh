@@ -255,9 +255,9 @@ template <int MAXT> struct Team {
     // (6 exchanges instead of 20); the warps' sums meet in the same way.
     template <int N> __device__ __forceinline__ void sum(float (&v)[N]) {
         static_assert(N >= 1 && N <= 4, "up to four values");
-        if constexpr (MAXT == 32) {
+        if (MAXT == 32 && blockDim.x < 32) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
+            for (int o = 8; o > 0; o >>= 1)
                 if (o < blockDim.x) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(mask, v[i], o);
@@ -282,6 +282,11 @@ template <int MAXT> struct Team {
 #pragma unroll
             for (; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
             // lane l has value l / L
+            if constexpr (MAXT == 32) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = NP == 1 ? k : __shfl_sync(0xffffffffu, k, i * L);
+                return;
+            }
             float* b = buf + flip * 4 * W;
             flip ^= 1;
             if (l % L == 0) b[l / L * W + (threadIdx.x >> 5)] = k;
