@@ -150,14 +150,16 @@ static Split split_rows(const prism_block_norm_t* n, bool one_group) {
     s.rpg = !one_group && n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
     s.groups = (n->rows + s.rpg - 1) / s.rpg;
     const int64_t teams = (int64_t)kSMs * sm_teams(n->channels, bwd_ctas(team_bucket(team_threads(n->channels))));
-    // of the teams a group's share by its rows: the last group may be shorter than the others
-    int64_t per = (s.groups * 4 <= teams ? teams : 8 * teams) * s.rpg / n->rows;
-    int64_t most = (s.rpg + 3) / 4;
-    if (s.groups * most < teams) most = (s.rpg + 1) / 2;      // little work: the shorter chain of rows counts more
+    const int64_t per_cta = cta_teams(n->channels), ctas = teams / per_cta;
+    // of the CTAs a group's share by its rows: the last group may be shorter than the others
+    int64_t per = (s.groups * 4 <= ctas ? ctas : 8 * ctas) * s.rpg / n->rows;
+    int64_t most = (s.rpg + 4 * per_cta - 1) / (4 * per_cta);
+    if (s.groups * most < ctas) most = (s.rpg + 2 * per_cta - 1) / (2 * per_cta);   // little work: the shorter chain counts
     if (per > most) per = most;
-    if (per > 1) {
-        s.per_group = (int)per;
-        s.segs = s.groups * per;
+    // a group that is not cut keeps the teams of a CTA busy only if it is long
+    if (per > 1 || (per_cta > 1 && s.rpg >= 8 && s.groups * 4 <= teams)) {
+        s.per_group = per < 1 ? 1 : (int)per;
+        s.segs = s.groups * s.per_group;
     } else {
         s.segs = s.groups < teams ? s.groups : teams;
     }

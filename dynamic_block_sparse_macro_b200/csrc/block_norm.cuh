@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fw
 }
 
 constexpr bool vec_shared(int maxt) { return maxt > 640; }
+constexpr int kTeamSums = 256 * 8 * 3 * (int)sizeof(float);       // of the teams of a CTA that are each within a warp
 
 // What the backward's branch is: none, one that goes to the sum as it is, or one with a norm of its own.  (Behind an rms
 // norm of the branch mean(dn ∘ nh) can be put together from sums that are known before dz', one barrier a row less;
@@ -313,16 +314,19 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
     Team<MAXT> team;
     team.init(sums);
     const int t = threadIdx.x, T = blockDim.x, C = a.C;
-    const int64_t seg = MAXT == 32 ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
+    // A segment is a CTA's.  Segment s of a group takes its rows s, s + per_group, ... (teams within a warp: in runs of
+    // a row a team), so that all teams move over the rows together.  Where groups are many and short a segment is a
+    // team's and has a run of them.
+    const bool whole = a.per_group == 0;
+    const int64_t seg = MAXT == 32 && whole ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
     if (seg >= a.segs) return;
-    // Segment s of a group takes its rows s, s + per_group, ...: all teams move over the rows together.  Where groups
-    // are many and short a segment has a run of them.
     int64_t g, r0, r1, step = 1;
-    if (a.per_group > 0) {
+    if (!whole) {
+        const int teams = MAXT == 32 ? blockDim.y : 1, me = MAXT == 32 ? threadIdx.y : 0;
         g = seg / a.per_group;
-        r0 = g * a.rpg + (seg - g * a.per_group);
+        r0 = g * a.rpg + (seg - g * a.per_group) * teams + me;
         r1 = (g + 1) * a.rpg;
-        step = a.per_group;
+        step = (int64_t)a.per_group * teams;
     } else {
         g = a.groups * seg / a.segs;
         r0 = g * a.rpg;
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
     int stage = 0;
     bool first = true;
     for (int64_t r = r0;;) {              // over the segment's groups
-        const int64_t end = a.per_group > 0 || (g + 1) * a.rpg > r1 ? r1 : (g + 1) * a.rpg;
+        const int64_t end = !whole || (g + 1) * a.rpg > r1 ? r1 : (g + 1) * a.rpg;
         F2 mul_[4], gate_[4];
         {
             float m[8], q[8];
@@ -579,7 +583,30 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
             f = both(sB[HAS_H ? i : 0]);
             fB[2 * i] = f.x; fB[2 * i + 1] = f.y;
         }
-        const bool whole = a.per_group == 0;
+        if (MAXT == 32 && !whole) {
+            // the CTA's teams add up through shared memory, whose rows have all been used
+            if (!a.part) break;
+            if constexpr (RING) cp_wait<0>();
+            __syncthreads();
+            float* all = reinterpret_cast<float*>(g_ring);
+            const int width = 8 * T;
+            float* mine = all + threadIdx.y * 3 * width;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = ((i / E) * T + t) * E + i % E;
+                mine[c] = fA[i];
+                mine[width + c] = fD[i];
+                if constexpr (HAS_H) mine[2 * width + c] = fB[i];
+            }
+            __syncthreads();
+            for (int i = threadIdx.y * T + t; i < (HAS_H ? 3 : 2) * width; i += 256) {
+                float v = 0.f;
+                for (int k = 0; k < (int)blockDim.y; ++k) v += all[k * 3 * width + i];
+                const int which = i / width, c = i - which * width;
+                if (c < C) a.part[(seg * 3 + which) * C + c] = v;
+            }
+            break;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = (u * T + t) * E;
@@ -659,7 +686,11 @@ inline int cta_teams(int C) {
 constexpr int team_bucket(int threads) {
     return threads <= 32 ? 32 : threads <= 256 ? 256 : threads <= 384 ? 384 : threads <= 512 ? 512 : threads <= 640 ? 640 : threads <= 768 ? 768 : 1024;
 }
-constexpr int fwd_ctas(int maxt, int unit) { return maxt == 32 ? 2 : maxt <= 256 ? (unit >= 4 ? 3 : 2) : maxt <= 384 ? 2 : 1; }
+constexpr int fwd_ctas(int maxt, int unit, bool branch) {
+    if (maxt <= 256) return maxt == 32 || unit < 4 ? 2 : 3;
+    if (!branch && unit >= 4) return maxt <= 384 ? 3 : maxt <= 768 ? 2 : 1;
+    return maxt <= 384 ? 2 : 1;
+}
 constexpr int bwd_ctas(int maxt) { return maxt <= 256 ? 2 : 1; }
 // teams that run at a time on an SM
 inline int sm_teams(int C, int ctas) {
@@ -676,7 +707,8 @@ prism_status_t launch_bwd_one(const BwdArgs& a, dim3 grid, dim3 block, cudaStrea
     constexpr int most = ((216 << 10) / CTAS - vec * threads) / (row * threads);
     constexpr int D = most < 1 ? 1 : most > kRowsAhead ? kRowsAhead : most;
     auto kernel = &k_block_norm_bwd<TX, TH, E, MAXT, H, CTAS, D>;
-    const int bytes = ((Lane<TX, E>::kAsync && Lane<TH, E>::kAsync ? D * row : 0) + vec) * (int)(block.x * block.y);
+    int bytes = ((Lane<TX, E>::kAsync && Lane<TH, E>::kAsync ? D * row : 0) + vec) * (int)(block.x * block.y);
+    if (MAXT == 32 && bytes < kTeamSums) bytes = kTeamSums;
     // with the static part, more than the 48 KB that need no leave
     if (bytes > 40 << 10 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return PRISM_ERR_CUDA;
@@ -686,7 +718,7 @@ prism_status_t launch_bwd_one(const BwdArgs& a, dim3 grid, dim3 block, cudaStrea
 template <typename TX, typename TH, int E, int MAXT, int H>
 prism_status_t launch_fwd_one(const FwdArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
     constexpr bool async = Lane<TX, E>::kAsync && Lane<TH, E>::kAsync && MAXT > 256;
-    constexpr int row = 8 * (int)(sizeof(TX) + (H != kNoBranch ? sizeof(TH) : 0)), ctas = fwd_ctas(MAXT, E);
+    constexpr int row = 8 * (int)(sizeof(TX) + (H != kNoBranch ? sizeof(TH) : 0)), ctas = fwd_ctas(MAXT, E, H != kNoBranch);
     constexpr int most = (216 << 10) / ctas / (row * MAXT), D = !async ? 0 : most > kRowsAhead ? kRowsAhead : most;
     auto kernel = &k_block_norm_fwd<TX, TH, E, MAXT, H != kNoBranch, ctas, D>;
     const int bytes = D * row * (int)block.x;
@@ -723,14 +755,14 @@ template <typename TX, typename TH> prism_status_t launch_bwd(const BwdArgs& a, 
     template <> prism_status_t launch_fwd<TX, TH>(const FwdArgs& a, int unit, cudaStream_t s) {        \
         const dim3 block(team_threads(a.C), cta_teams(a.C));                                           \
         const int64_t want = (a.R + block.y - 1) / block.y;                                            \
-        const int64_t most = kSMs * (int64_t)sm_teams(a.C, fwd_ctas(team_bucket(block.x), unit)) / block.y;  \
+        const int64_t most = kSMs * (int64_t)sm_teams(a.C, fwd_ctas(team_bucket(block.x), unit, a.h != nullptr)) / block.y;  \
         const dim3 grid((unsigned)(want < most ? want : most));                                        \
         if (a.h) PRISM_BN_BY_UNIT(launch_fwd_one, TX, TH, kPlain);                                     \
         else PRISM_BN_BY_UNIT(launch_fwd_one, TX, TH, kNoBranch);                                      \
     }                                                                                                  \
     template <> prism_status_t launch_bwd<TX, TH>(const BwdArgs& a, int unit, cudaStream_t s) {        \
         const dim3 block(team_threads(a.C), cta_teams(a.C));                                           \
-        const dim3 grid((unsigned)((a.segs + block.y - 1) / block.y));                                 \
+        const dim3 grid((unsigned)(a.per_group > 0 ? a.segs : (a.segs + block.y - 1) / block.y));      \
         if (a.h && a.post != PRISM_NORM_NONE) PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kNormed);       \
         else if (a.h) PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kPlain);                                \
         else PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kNoBranch);                                      \

@@ -69,6 +69,7 @@ def test_norm_arguments_refused(L):
     assert bwd(L, n, dgate=P) == bwd(L, n, dw=P) == bwd(L, n, db=P) == bwd(L, n, dscale=P) == ARG   # without the vector
     assert bwd(L, n, w_post=P) == ARG
     assert bwd(L, norm_desc(norm=0), dz=None, dy=None) == ARG
+    n = norm_desc(rows=100, rows_per_group=50)                       # cut groups: their sums meet in the workspace
     assert bwd(L, n, dshift=P) == WS and bwd(L, n, dshift=P, ws=P, ws_bytes=64) == WS
     assert bwd(L, n, dshift=P, ws=P + 4, ws_bytes=1 << 30) == ARG
     assert fwd(L, norm_desc(rows=0), x=None, h=P, z=None, y=None) == OK     # no rows: nothing launched
@@ -77,14 +78,17 @@ def test_norm_arguments_refused(L):
 def test_norm_workspace_grows_with_the_split_only(L):
     def size(**kw):
         return _abi.block_norm_ws_bytes(norm_desc(**kw))
-    # [segments][3][C] floats; a row alone is one segment, and segments have two rows at least
+    # [segments][3][C] floats.  64 channels: CTAs of 32 teams of 8 threads, two an SM; segments of two rows a team at least
     assert size(rows=1) == 1 * 3 * 64 * 4
-    assert size(rows=8, rows_per_group=8) == 4 * 3 * 64 * 4
-    # 64 channels: teams of 8 threads, two CTAs of 32 teams an SM
-    assert size(rows=10 ** 6, rows_per_group=10 ** 6) == 148 * 64 * 3 * 64 * 4
+    assert size(rows=128, rows_per_group=128) == 2 * 3 * 64 * 4
+    assert size(rows=10 ** 6, rows_per_group=10 ** 6) == 296 * 3 * 64 * 4
     # groups of one row are not cut, and shared out among the teams
     assert size(rows=1000, rows_per_group=1) == 1000 * 3 * 64 * 4
     assert size(rows=10 ** 5, rows_per_group=1) == 148 * 64 * 3 * 64 * 4
+    # 2048 channels: a team a CTA
+    assert size(rows=1, channels=2048) == 1 * 3 * 2048 * 4
+    assert size(rows=8, rows_per_group=8, channels=2048) == 4 * 3 * 2048 * 4
+    assert size(rows=61440, rows_per_group=30720, channels=2048) == 296 * 3 * 2048 * 4
 
 
 def rot_desc(**kw):
