@@ -237,7 +237,7 @@ extern "C" prism_status_t prism_block_norm_fwd(const prism_block_norm_t* n, cons
     a.R = n->rows;
     a.rpg = n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
     a.C = C; a.norm = n->norm; a.post = n->post_norm; a.eps = n->eps; a.res = n->res_scale;
-    const int unit = unit_of(es == 2 ? 8 : 4, C, {a.ld_x, h ? a.ld_h : 0, h ? a.ld_z : 0, has_y ? a.ld_y : 0, gate ? a.ld_gate : 0,
+    const int unit = unit_of(eb == 2 ? 8 : 4, C, {a.ld_x, h ? a.ld_h : 0, h ? a.ld_z : 0, has_y ? a.ld_y : 0, gate ? a.ld_gate : 0,
                                  scale ? a.ld_scale : 0, shift ? a.ld_shift : 0},
                              {x, h, gate, w_post, w, b, scale, shift, z, y});
     if (n->stream_dtype == PRISM_BF16) st = launch_fwd<__nv_bfloat16, __nv_bfloat16>(a, unit, stream);

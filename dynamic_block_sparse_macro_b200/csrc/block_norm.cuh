@@ -670,8 +670,10 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
     let_next_start();
 }
 
-// channels of the widest access: 16 bytes of the stream, so that a warp's access leaves no gaps
-template <typename TX> constexpr int wide_unit() { return 16 / (int)sizeof(TX); }
+// Channels of the widest access, where stream and branch differ: 16 bytes of the branch forwards (f32 and bf16,
+// 61440 x 2048: 236 us, 16 bytes of the stream 243), and of the stream backwards (372; of the branch 477: a lane's
+// eight floats are then two copies that leave gaps in a warp's access).
+template <typename T> constexpr int wide_unit() { return 16 / (int)sizeof(T); }
 // threads of a team: 8 channels a thread; 8, 16 or a whole number of warps
 inline int team_threads(int C) {
     const int n = (C + 7) / 8;
@@ -743,9 +745,9 @@ template <typename TX, typename TH> prism_status_t launch_bwd(const BwdArgs& a, 
         default: return ONE<TX, TH, E, 1024, H>(a, grid, block, s);                   \
     }
 
-#define PRISM_BN_BY_UNIT(ONE, TX, TH, H)                                              \
+#define PRISM_BN_BY_UNIT(ONE, TW, TX, TH, H)                                          \
     do {                                                                              \
-        constexpr int kWide = wide_unit<TX>();                                        \
+        constexpr int kWide = wide_unit<TW>();                                        \
         if (unit == kWide) PRISM_BN_BY_SIZE(ONE, TX, TH, kWide, H)                    \
         if (unit == 2) PRISM_BN_BY_SIZE(ONE, TX, TH, 2, H)                            \
         PRISM_BN_BY_SIZE(ONE, TX, TH, 1, H)                                           \
@@ -757,15 +759,15 @@ template <typename TX, typename TH> prism_status_t launch_bwd(const BwdArgs& a, 
         const int64_t want = (a.R + block.y - 1) / block.y;                                            \
         const int64_t most = kSMs * (int64_t)sm_teams(a.C, fwd_ctas(team_bucket(block.x), unit, a.h != nullptr)) / block.y;  \
         const dim3 grid((unsigned)(want < most ? want : most));                                        \
-        if (a.h) PRISM_BN_BY_UNIT(launch_fwd_one, TX, TH, kPlain);                                     \
-        else PRISM_BN_BY_UNIT(launch_fwd_one, TX, TH, kNoBranch);                                      \
+        if (a.h) PRISM_BN_BY_UNIT(launch_fwd_one, TH, TX, TH, kPlain);                                     \
+        else PRISM_BN_BY_UNIT(launch_fwd_one, TH, TX, TH, kNoBranch);                                      \
     }                                                                                                  \
     template <> prism_status_t launch_bwd<TX, TH>(const BwdArgs& a, int unit, cudaStream_t s) {        \
         const dim3 block(team_threads(a.C), cta_teams(a.C));                                           \
         const dim3 grid((unsigned)(a.per_group > 0 ? a.segs : (a.segs + block.y - 1) / block.y));      \
-        if (a.h && a.post != PRISM_NORM_NONE) PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kNormed);       \
-        else if (a.h) PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kPlain);                                \
-        else PRISM_BN_BY_UNIT(launch_bwd_one, TX, TH, kNoBranch);                                      \
+        if (a.h && a.post != PRISM_NORM_NONE) PRISM_BN_BY_UNIT(launch_bwd_one, TX, TX, TH, kNormed);       \
+        else if (a.h) PRISM_BN_BY_UNIT(launch_bwd_one, TX, TX, TH, kPlain);                                \
+        else PRISM_BN_BY_UNIT(launch_bwd_one, TX, TX, TH, kNoBranch);                                      \
     }
 
 }  // namespace bn
