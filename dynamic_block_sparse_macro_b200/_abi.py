@@ -412,25 +412,12 @@ def prism_sparse_attn_bwd_raster_ds(prob, Q, K, V, o_f32, dO, lse, perm, shape_i
 
 
 # ---------------------------------------------------------------- around the attention
-# Descriptors are passed by address (ctypes.addressof of a kept structure).
+# Descriptors are passed by address (ctypes.addressof of a kept structure); block.py makes the calls themselves, with
+# the descriptors and addresses that it keeps.
 def block_norm_ws_bytes(n: BlockNormT) -> int:
     out = ctypes.c_size_t(0)
     _check("prism_block_norm_ws_bytes", lib().prism_block_norm_ws_bytes(ctypes.addressof(n), ctypes.addressof(out)))
     return out.value
-
-
-def prism_block_norm_fwd(n: BlockNormT, x, h, gate, w_post, w, b, scale, shift, z, y, stream=None):
-    _check("prism_block_norm_fwd", lib().prism_block_norm_fwd(
-        ctypes.addressof(n), _ptr(x), _ptr(h), _ptr(gate), _ptr(w_post), _ptr(w), _ptr(b), _ptr(scale), _ptr(shift),
-        _ptr(z), _ptr(y), _stream(stream)))
-
-
-def prism_block_norm_bwd(n: BlockNormT, z, h, gate, w_post, w, b, scale, dz, dy, dx, dh, dgate, dw_post, dw, db, dscale,
-                         dshift, ws, ws_bytes, stream=None):
-    _check("prism_block_norm_bwd", lib().prism_block_norm_bwd(
-        ctypes.addressof(n), _ptr(z), _ptr(h), _ptr(gate), _ptr(w_post), _ptr(w), _ptr(b), _ptr(scale), _ptr(dz),
-        _ptr(dy), _ptr(dx), _ptr(dh), _ptr(dgate), _ptr(dw_post), _ptr(dw), _ptr(db), _ptr(dscale), _ptr(dshift),
-        _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def head_rotate_ws_bytes(p: RotateT) -> int:
@@ -439,45 +426,9 @@ def head_rotate_ws_bytes(p: RotateT) -> int:
     return out.value
 
 
-def prism_head_rotate_fwd(p: RotateT, Q, K, wq, wk, table, Qr, Kr, stream=None):
-    _check("prism_head_rotate_fwd", lib().prism_head_rotate_fwd(
-        ctypes.addressof(p), _ptr(Q), _ptr(K), _ptr(wq), _ptr(wk), _ptr(table), _ptr(Qr), _ptr(Kr), _stream(stream)))
-
-
-def prism_head_rotate_bwd(p: RotateT, Q, K, wq, wk, table, dQr, dKr, dQ, dK, dwq, dwk, ws, ws_bytes, stream=None):
-    _check("prism_head_rotate_bwd", lib().prism_head_rotate_bwd(
-        ctypes.addressof(p), _ptr(Q), _ptr(K), _ptr(wq), _ptr(wk), _ptr(table), _ptr(dQr), _ptr(dKr), _ptr(dQ), _ptr(dK),
-        _ptr(dwq), _ptr(dwk), _ptr(ws), ws_bytes, _stream(stream)))
-
-
 def expert_sizes(e: ExpertsT) -> tuple:
     """(rows of a sorted buffer, workspace bytes of the plan)."""
     rows, ws = ctypes.c_int64(0), ctypes.c_size_t(0)
     _check("prism_expert_sizes", lib().prism_expert_sizes(ctypes.addressof(e), ctypes.addressof(rows),
                                                           ctypes.addressof(ws)))
     return rows.value, ws.value
-
-
-def prism_expert_plan(e: ExpertsT, ids, counts, offsets, pos, src, ws, ws_bytes, stream=None):
-    _check("prism_expert_plan", lib().prism_expert_plan(
-        ctypes.addressof(e), _ptr(ids), _ptr(counts), _ptr(offsets), _ptr(pos), _ptr(src), _ptr(ws), ws_bytes,
-        _stream(stream)))
-
-
-def prism_expert_dispatch(e: ExpertsT, dtype, channels, x, ld_x, pos, counts, offsets, clear_tail, xs, stream=None):
-    _check("prism_expert_dispatch", lib().prism_expert_dispatch(
-        ctypes.addressof(e), dtype, channels, _ptr(x), ld_x, _ptr(pos), _ptr(counts), _ptr(offsets), clear_tail, _ptr(xs),
-        _stream(stream)))
-
-
-def prism_expert_combine(e: ExpertsT, dtype, channels, y, pos, weights, add, ld_add, out, ld_out, stream=None):
-    _check("prism_expert_combine", lib().prism_expert_combine(
-        ctypes.addressof(e), dtype, channels, _ptr(y), _ptr(pos), _ptr(weights), _ptr(add), ld_add, _ptr(out), ld_out,
-        _stream(stream)))
-
-
-def prism_expert_combine_bwd(e: ExpertsT, dtype, channels, dout, ld_dout, y, pos, weights, counts, offsets, clear_tail,
-                             dy, dweights, stream=None):
-    _check("prism_expert_combine_bwd", lib().prism_expert_combine_bwd(
-        ctypes.addressof(e), dtype, channels, _ptr(dout), ld_dout, _ptr(y), _ptr(pos), _ptr(weights), _ptr(counts),
-        _ptr(offsets), clear_tail, _ptr(dy), _ptr(dweights), _stream(stream)))

@@ -11,7 +11,11 @@
 //
 // The moves are bound by HBM.  All of them go by token: a token's row is read or written once however many
 // experts it has, and no two threads add to one value, so nothing is atomic and sums have a fixed order
-// (j ascending, in fp32, one rounding at the store).
+// (j ascending, in fp32, one rounding at the store).  61440 x 2048 bf16, two choices: dispatch 114 us (117 at the
+// measured copy rate), combine 113 (117), its backward 205 (194); 32768 x 1024, eight choices: dispatch 99 (93),
+// combine 97 (93).
+// The plan is bound by latency: a count of each CTA's slots and a placement, 11 us for 122880 slots of 16 experts, 21
+// for 262144 of 128; by one CTA 6147 slots took 13 us, by two launches 10.
 #include <initializer_list>
 
 #include "rows.cuh"

@@ -188,6 +188,7 @@ template <typename T, int E> struct Lane {
     }
     // places that no copy writes (past the row's end, or `all`) hold 0
     static __device__ __forceinline__ void clear(char* s, int threads, int tid, int t, int team, int C, bool all) {
+        if (!all && ((U - 1) * team + t) * E < C) return;
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (all || (u * team + t) * E >= C) {

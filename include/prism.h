@@ -494,6 +494,7 @@ size_t prism_layer_sizeof(void);
  *    on 16 bytes is moved by narrower accesses.  Workspaces and the rotation's
  *    pointers and strides are on 16 bytes.
  *  - All arithmetic is fp32; a bf16 result is rounded once, when stored.
+ *    Squares of what is normed have to stay in fp32's range.
  *  - No call uses atomics on floating-point values: results do not depend on
  *    scheduling.  A workspace may be reused as soon as the call's stream has
  *    passed it; two calls that may overlap (two streams, two captured graphs)

@@ -290,3 +290,48 @@ def test_columns_of_one_buffer_are_apart():
     assert not block._apart(b[:, :9], b[:, 8:16]) and not block._apart(b[:4], b[3:])
     assert block._apart(b[:3], b[3:]) and not block._apart(b[1:, :8], b.view(-1, 12)[:, :8])
     assert not block._apart(b[:3, 20:], b.view(-1)[20:20 + 72].view(3, 24)[:, :8])     # runs over the row's end
+
+
+def test_calls_move_to_the_tensors_device(L, host, monkeypatch):
+    """A call on tensors of another device than the current one is made with theirs as the current one."""
+    current = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            current[0] = "theirs"
+
+        def __exit__(self, *a):
+            current[0] = 0
+
+    class Reached(Exception):
+        pass
+
+    def stream(index):
+        assert current[0] == "theirs"
+        raise Reached
+    monkeypatch.setattr(block, "_current", lambda index: current[0] == "theirs")
+    monkeypatch.setattr(block, "_stream", stream)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    x, t = torch.zeros(6, 8), torch.zeros(62, 2)
+    q = torch.zeros(6, 2, 64)
+    kw = dict(grid=(1, 2, 3), axes=(12, 10, 10))
+    p = block.ExpertPlan(6, 2, 3, 1, 8, torch.device("cpu"))
+    ys = torch.zeros(p.rows_sorted, 8)
+    for f in (lambda: block.norm_forward(x, x), lambda: block.norm_backward(x, x, x, x),
+              lambda: block.rotate_forward(q, None, t, **kw), lambda: block.rotate_backward(q, None, q, None, t, **kw),
+              lambda: block.expert_plan(torch.zeros(6, 2, dtype=torch.int64), 3), lambda: block.expert_dispatch(x, p),
+              lambda: block.expert_combine(ys, p), lambda: block.expert_combine_backward(x, ys, p)):
+        with pytest.raises(Reached):
+            f()
+        assert current[0] == 0
+
+
+def test_kept_signatures_are_bounded(monkeypatch):
+    monkeypatch.setattr(block, "_plans", {})
+    monkeypatch.setattr(block, "_MAX_PLANS", 3)
+    for i in range(10):
+        block._keep(i, i)
+        assert len(block._plans) <= 3 and block._plans[i] == i

@@ -201,6 +201,59 @@ def test_norm_in_place_and_empty_and_constant_rows():
     assert bool((block.norm_forward(torch.zeros_like(c), norm="rms")[1] == 0).all())
 
 
+def test_norm_of_one_channel_one_row_and_other_shapes():
+    n = gen(13)
+    # one channel: nothing is left of it after a layer norm but the shift
+    x, b = n(5, 1), n(1)
+    assert torch.equal(block.norm_forward(x, bias=b)[1], b.expand(5, 1))
+    g = block.norm_backward(x, None, None, n(5, 1), bias=b)
+    assert bool((g["dx"] == 0).all())
+    # a vector alone, and rows of a view with leading dimensions that cannot be walked
+    v = n(64)
+    want = block.norm_forward(v.view(1, 64), norm="rms")[1]
+    assert torch.equal(block.norm_forward(v, norm="rms")[1], want.view(64))
+    w = n(4, 3, 5, 64, dt=BF16)
+    for t in (w, w.transpose(0, 2), w[:, :, ::2], w.transpose(2, 3).contiguous().transpose(2, 3)):
+        z, y = block.norm_forward(t, t, norm="rms")
+        z0, y0 = block.norm_forward(t.contiguous().view(-1, 64), t.contiguous().view(-1, 64), norm="rms")
+        assert z.shape == t.shape and torch.equal(z.reshape(-1, 64), z0) and torch.equal(y.reshape(-1, 64), y0)
+        g = block.norm_backward(t, t, t, t, norm="rms")
+        g0 = block.norm_backward(*(t.contiguous().view(-1, 64),) * 4, norm="rms")
+        assert torch.equal(g["dx"].reshape(-1, 64), g0["dx"])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows' bits are those of a call on them alone."""
+    R, C = 524289 + 37, 4096
+    x = torch.empty(R, C, dtype=BF16, device="cuda")
+    x.view(-1)[: 1 << 20].normal_()
+    x[-100:].normal_()
+    x[-200:-100].fill_(0)
+    w = 1 + gen(14)(C, std=0.2)
+    y = block.norm_forward(x, weight=w)[1]
+    assert torch.equal(y[-50:], block.norm_forward(x[-50:].contiguous(), weight=w)[1])
+    g = block.norm_backward(x, None, None, y, wants=(), weight=w)["dx"]
+    assert torch.equal(g[-50:], block.norm_backward(x[-50:].contiguous(), None, None, y[-50:].contiguous(), wants=(),
+                                                    weight=w)["dx"])
+    del g
+    ids = torch.arange(R, device="cuda").view(R, 1) % 3
+    plan = block.expert_plan(ids, 3)
+    xs = block.expert_dispatch(x, plan, out=y)                    # every row of it has a slot
+    assert torch.equal(xs[plan.pos[-50:, 0].long()], x[-50:])
+    out = block.expert_combine(xs, plan)
+    assert torch.equal(out[-50:], x[-50:]) and torch.equal(out[:50], x[:50])
+    del out, xs, y
+    q = x[:262144 + 9].view(-1, 32, 128)[:524288 + 16]            # 2^31 + 2^16 elements
+    grid, axes = (8, 32, 32), (22, 21, 21)
+    table = block.rotation_table(grid, axes)
+    qr = block.rotate_forward(q, None, table, grid=grid, axes=axes)[0]
+    tail = q[-16:].contiguous()
+    at = (torch.arange(q.shape[0] - 16, q.shape[0]) % 8192)
+    full = torch.zeros(8192, 32, 128, dtype=BF16, device="cuda")
+    full[at] = tail
+    assert torch.equal(qr[-16:], block.rotate_forward(full, None, table, grid=grid, axes=axes)[0][at])
+
+
 def test_norm_row_with_nan_stays_alone():
     n = gen(10)
     x = n(64, 256)
