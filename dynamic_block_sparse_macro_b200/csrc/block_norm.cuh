@@ -21,10 +21,11 @@
 // row's end enters no sum.  Of what decides the speed:
 //   - no spills: the f32 / bf16 forward at 131072 x 2048 took 705 us with 88 bytes of them and takes 501 without (498
 //     at the measured copy rate); with more CTAs an SM (64 registers, 112 bytes) 747;
-//   - fp32 pairs in one instruction: the backward of 61440 x 2048 339 -> 248 us (233), rows copied three ahead included;
-//   - teams of more than 512 threads have an SM to themselves and leave it idle at each of a row's two or three
-//     barriers: 8191 x 5120 with two rms norms 110 us (78), 13269 x 8192 276 (202).  Clusters of CTAs of 256 threads
-//     in their place wait longer for the cluster's barrier: 13269 x 4096 229 us instead of 128.
+//   - fp32 pairs in one instruction: the backward of 61440 x 2048 339 -> 248 us, rows copied three ahead included; with
+//     one barrier a row less 243 (233);
+//   - teams of more than 256 threads have an SM to themselves and leave it idle at each of a row's barriers: 8191 x 5120
+//     with two rms norms 98 us (78), 13269 x 8192 276 (202).  Clusters of CTAs of 256 threads in their place wait longer
+//     for one another: 13269 x 4096 149 us instead of 128, with the cluster's own barrier 229.
 //   - rows of odd width move element by element: 40000 x 1001 bf16 218 us backwards, x 1000 93.
 #pragma once
 
@@ -250,7 +251,53 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fw
     vectors(g);
 
     int stage = 0;
-    for (int64_t r = r0; r < r1; r += step) {
+    int64_t r = r0;
+    if constexpr (RING && D >= 2 && !HAS_H) {
+        if (a.norm == PRISM_NORM_LAYER) {
+            // A row's second sum goes together with the next row's first one, one barrier a row less: 13269 x 5416
+            // 82 -> 72 us.  (With a branch, whose rows are then summed up twice, 4096 wide 84 -> 88.)
+            auto stream = [&](F2 (&v)[4], int st) { LX::read(v, g_ring + st * stage_bytes, T, t); };
+            auto total = [&](const F2 (&v)[4]) { return sum((v[0] + v[1]) + (v[2] + v[3])); };
+            while (r < r1) {
+                if (r >= next) {
+                    vectors(++g);
+                    next += a.rpg;
+                }
+                const int64_t end = next < r1 ? next : r1;
+                F2 v[4];
+                cp_wait<D - 1>();
+                stream(v, stage);
+                float m = team.sum1(total(v));
+                for (; r < end; r += step) {
+                    const int after = stage + 1 == D ? 0 : stage + 1;
+                    stream(v, stage);
+                    m = -mean_of(m, fc, inv_c);
+                    F2 q;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = v[i] + pair(m, i);
+                        q = i ? fma(v[i], v[i], q) : v[i] * v[i];
+                    }
+                    float two[2] = {sum(q), 0.f};
+                    if (r + step < end) {
+                        F2 ahead[4];
+                        cp_wait<D - 2>();
+                        stream(ahead, after);
+                        two[1] = total(ahead);
+                    }
+                    team.sum(two);
+                    const F2 rs = f2(rsqrtf(two[0] * inv_c + a.eps));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = fma(v[i] * rs, mul[i], add[i]);
+                    put_units<TH, E>((TH*)a.y + r * a.ld_y, v, t, T, C);
+                    fetch(r + D * step, stage);
+                    stage = after;
+                    m = two[1];
+                }
+            }
+        }
+    }
+    for (; r < r1; r += step) {
         F2 v[4], hv[HAS_H ? 4 : 1];
         if constexpr (RING) {
             cp_wait<D - 1>();
@@ -307,9 +354,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fw
 constexpr bool vec_shared(int maxt) { return maxt > 640; }
 constexpr int kTeamSums = 256 * 8 * 3 * (int)sizeof(float);       // of the teams of a CTA that are each within a warp
 
-// What the backward's branch is: none, one that goes to the sum as it is, or one with a norm of its own.  (Behind an rms
-// norm of the branch mean(dn ∘ nh) can be put together from sums that are known before dz', one barrier a row less;
-// with its four more sums 8191 x 5120 took 127 us instead of 110.)
+// What the backward's branch is: none, one that goes to the sum as it is, or one with a norm of its own.
 enum Branch { kNoBranch = 0, kPlain = 1, kNormed = 2 };
 
 template <typename TX, typename TH, int E, int MAXT, int BR, int CTAS, int D>
@@ -470,6 +515,156 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
             if constexpr (HAS_H) sB[i] = f2(0.f);
         }
 
+        // Teams of several warps take two rows at a time in part, so that a row has one barrier less: what the one's last
+        // sum and the other's first one add up goes together.  The second row's values are read twice from the ring.
+        // 61440 x 2048, layer norm: 251 -> 243 us, 13269 x 4096 128 -> 117; 8191 x 5120, two rms norms: 109 -> 98.
+        [[maybe_unused]] auto store_dx = [&](int64_t row, const F2 (&d)[4]) {
+            F2 o[4];
+            const F2 res = f2(HAS_H ? a.res : 1.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = HAS_H ? d[i] * res : d[i];
+            put_units<TX, E>((TX*)a.dx + row * a.ld_dx, o, t, T, C);
+        };
+        if constexpr (RING && D >= 2 && MAXT > 32 && MAXT < 1024) {      // with 64 registers it spills
+            const char* base = g_ring;
+            if constexpr (BR == kNormed) {
+                if (!whole && a.norm == PRISM_NORM_RMS && a.post == PRISM_NORM_RMS) {
+                    F2 d[4], h[4];
+                    float rh_ = 0.f, last = 0.f;               // of the row before: 1/rms of h, sum of dn ∘ nh
+                    for (bool have = false;; have = true) {
+                        const bool more = r < end;
+                        if (!more && !have) break;
+                        const char* s = base + stage * stage_bytes;
+                        float v[4] = {last, 0.f, 0.f, 0.f};
+                        if (more) {
+                            cp_wait<D - 1>();
+                            F2 z[4], dy[4], x[4], mul[4], q[3];
+                            LX::read(z, s, threads, tid);
+                            LH::read(dy, s + o_dy, threads, tid);
+                            LH::read(x, s + o_h, threads, tid);
+                            get(mul, mul_, 0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const F2 c = dy[i] * mul[i];
+                                q[0] = i ? fma(z[i], z[i], q[0]) : z[i] * z[i];
+                                q[1] = i ? fma(c, z[i], q[1]) : c * z[i];
+                                q[2] = i ? fma(x[i], x[i], q[2]) : x[i] * x[i];
+                            }
+#pragma unroll
+                            for (int i = 0; i < 3; ++i) v[1 + i] = sum(q[i]);
+                        }
+                        team.sum(v);
+                        if (have) {
+                            const F2 mdn = f2(-v[0] * inv_c), rr = f2(rh_);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) d[i] = rr * fma(h[i], mdn, d[i]);
+                            put_units<TH, E>((TH*)a.dh + (r - step) * a.ld_dh, d, t, T, C);
+                        }
+                        if (!more) break;
+                        const float rs = rsqrtf(v[1] * inv_c + a.eps), mcn = v[2] * rs * inv_c;
+                        rh_ = rsqrtf(v[3] * inv_c + a.eps);
+                        {
+                            F2 z[4], dy[4], mul[4];
+                            LX::read(z, s, threads, tid);
+                            LH::read(dy, s + o_dy, threads, tid);
+                            LX::read(d, s + o_dz, threads, tid);
+                            get(mul, mul_, 0);
+                            const F2 rs2 = f2(rs), mcn2 = f2(-mcn);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const F2 n = z[i] * rs2;
+                                sA[i] = fma(dy[i], n, sA[i]);
+                                sD[i] = sD[i] + dy[i];
+                                d[i] = fma(rs2, fma(n, mcn2, dy[i] * mul[i]), d[i]);
+                            }
+                        }
+                        store_dx(r, d);
+                        F2 gate[4], q = f2(0.f);
+                        LH::read(h, s + o_h, threads, tid);
+                        get(gate, gate_, 1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            h[i] = h[i] * f2(rh_);
+                            sB[i] = fma(d[i], h[i], sB[i]);
+                            d[i] = d[i] * gate[i];
+                            q = fma(d[i], h[i], q);
+                        }
+                        last = sum(q);
+                        fetch(r + D * step, stage);
+                        stage = stage + 1 == D ? 0 : stage + 1;
+                        r += step;
+                    }
+                }
+            } else {
+                if (!whole && a.norm == PRISM_NORM_LAYER && r < end) {
+                    // sums of z and of c = dy ∘ mul over the row in the ring at s
+                    auto first_sums = [&](const char* s, float* v) {
+                        F2 z[4], dy[4], mul[4];
+                        LX::read(z, s, threads, tid);
+                        LH::read(dy, s + o_dy, threads, tid);
+                        get(mul, mul_, 0);
+                        F2 q = dy[0] * mul[0];
+#pragma unroll
+                        for (int i = 1; i < 4; ++i) q = fma(dy[i], mul[i], q);
+                        v[0] = sum((z[0] + z[1]) + (z[2] + z[3]));
+                        v[1] = sum(q);
+                    };
+                    float m[2];
+                    cp_wait<D - 1>();
+                    first_sums(base + stage * stage_bytes, m);
+                    team.sum(m);
+                    for (; r < end; r += step) {
+                        const char* s = base + stage * stage_bytes;
+                        const int after = stage + 1 == D ? 0 : stage + 1;
+                        const float mz = -mean_of(m[0], fc, inv_c), mc = m[1] * inv_c;
+                        F2 z[4], dy[4], mul[4], q[2];
+                        LX::read(z, s, threads, tid);
+                        LH::read(dy, s + o_dy, threads, tid);
+                        get(mul, mul_, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            z[i] = z[i] + pair(mz, i);
+                            q[0] = i ? fma(z[i], z[i], q[0]) : z[i] * z[i];
+                            q[1] = i ? fma(dy[i] * mul[i], z[i], q[1]) : dy[i] * mul[i] * z[i];
+                        }
+                        float v[4] = {sum(q[0]), sum(q[1]), 0.f, 0.f};
+                        if (r + step < end) {
+                            cp_wait<D - 2>();
+                            first_sums(base + after * stage_bytes, v + 2);
+                        }
+                        team.sum(v);
+                        const float rs = rsqrtf(v[0] * inv_c + a.eps), mcn = v[1] * rs * inv_c;
+                        const F2 rs2 = f2(rs), mcn2 = f2(-mcn);
+                        F2 d[4];
+                        LX::read(d, s + o_dz, threads, tid);
+                        if constexpr (VSM) get(mul, mul_, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const F2 n = z[i] * rs2;
+                            sA[i] = fma(dy[i], n, sA[i]);
+                            sD[i] = sD[i] + dy[i];
+                            d[i] = fma(rs2, fma(n, mcn2, fma(dy[i], mul[i], pair(-mc, i))), d[i]);
+                        }
+                        store_dx(r, d);
+                        if constexpr (HAS_H) {
+                            F2 h[4], gate[4];
+                            LH::read(h, s + o_h, threads, tid);
+                            get(gate, gate_, 1);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                sB[i] = fma(d[i], h[i], sB[i]);
+                                d[i] = d[i] * gate[i];
+                            }
+                            put_units<TH, E>((TH*)a.dh + r * a.ld_dh, d, t, T, C);
+                        }
+                        fetch(r + D * step, stage);
+                        stage = after;
+                        m[0] = v[2];
+                        m[1] = v[3];
+                    }
+                }
+            }
+        }
         for (; r < end; r += step) {
             F2 z[4], dy[4], d[4], h[HAS_H ? 4 : 1];
             if constexpr (RING) {
@@ -548,13 +743,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
                     }
                 }
             }
-            {
-                F2 o[4];
-                const F2 res = f2(HAS_H ? a.res : 1.f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = HAS_H ? d[i] * res : d[i];
-                put_units<TX, E>((TX*)a.dx + r * a.ld_dx, o, t, T, C);
-            }
+            store_dx(r, d);
             if constexpr (HAS_H) {
                 F2 q[2], gate[4];
                 get(gate, gate_, 1);

@@ -63,6 +63,12 @@ NORM_CASES = [
     (4099, 64, 1, BF16, BF16, "layer", None, "gate scale shift", 1.0),
     (3001, 72, 1500, BF16, BF16, None, "rms", "gate post_weight", 1.0),
     (2500, 128, 2500, F32, F32, "rms", None, "weight", 1.0),
+    # teams of several warps whose rows share barriers: one norm behind a plain branch, two rms norms; many rows a team
+    (997, 4096, 997, BF16, BF16, "layer", None, "gate scale shift", 1.0),
+    (1500, 3000, 499, F32, BF16, "rms", "rms", "gate post_weight weight", 0.5),
+    (611, 6000, 611, F32, F32, "layer", None, "gate weight bias scale shift", -1.0),
+    (2111, 264, 700, BF16, BF16, "rms", "rms", ALL, 1.0),
+    (4999, 1100, 4999, F32, F32, "layer", None, "scale shift", 1.0),
     # groups that are not cut, more of them than teams: runs of groups with all gradients
     (10007, 64, 1, F32, F32, "layer", "rms", ALL, 1.0),
     (1203, 2048, 2, BF16, BF16, "layer", "layer", ALL, 0.5),
