@@ -53,6 +53,7 @@ def _ptr(t):
 
 
 def _keep(key, plan):
+    """Keeps a finished plan: another thread may take it at once."""
     if len(_plans) >= _MAX_PLANS:
         _plans.clear()
     _plans[key] = plan
@@ -178,7 +179,7 @@ def _check_out(out, what, allowed, *others):
 
 def _refuse_capture(name, instead):
     if torch.cuda.is_current_stream_capturing():
-        raise RuntimeError(f"{name} records an autograd graph and cannot be captured; capture {instead}")
+        raise RuntimeError(f"{name} works on an autograd graph and cannot be captured; capture {instead}")
 
 
 def _wants_graph(*tensors):
@@ -193,7 +194,7 @@ def _vector(v, shape, what):
     _need(tuple(v.shape) == shape, f"{what} must be {shape}, not {tuple(v.shape)}")
 
 
-def _norm_plan(key, x, h, gate, post_weight, weight, bias, scale, shift, norm, post_norm, eps, res_scale, rows_per_group,
+def _norm_plan(x, h, gate, post_weight, weight, bias, scale, shift, norm, post_norm, eps, res_scale, rows_per_group,
                branch, rows):
     """The call's plan; ``rows``: its other tensors like x, as (field of the descriptor, name, tensor, type)."""
     _need(norm in _NORMS, f"norm is 'layer', 'rms' or None, not {norm!r}")
@@ -232,7 +233,7 @@ def _norm_plan(key, x, h, gate, post_weight, weight, bias, scale, shift, norm, p
     p = _Plan(desc, dev, copy)
     p.ws_bytes = _abi.block_norm_ws_bytes(desc)
     p.a, p.b = _NORMS[norm] != 0, (G, C)
-    return _keep(key, p)
+    return p
 
 
 def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=None, scale=None, shift=None,
@@ -255,9 +256,10 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
         _need(y is None or norm not in (None, "none"), "without a norm there is no y to write")
         for t, what in ((z, "z"), (y, "y")):
             _need(t is None or t.dim() < 1 or _row_stride(t) is not None, f"{what}'s rows must lie evenly")
-        p = _norm_plan(key, x, h, gate, post_weight, weight, bias, scale, shift, norm, post_norm, eps, res_scale,
+        p = _norm_plan(x, h, gate, post_weight, weight, bias, scale, shift, norm, post_norm, eps, res_scale,
                        rows_per_group, branch, (("z", "z", z, x.dtype), ("y", "y", y, branch)))
         p.c = branch
+        _keep(key, p)
     if p.copy:
         x0 = x
         vecs = [None if v is None else v.contiguous() for v in (post_weight, weight, bias)]
@@ -311,9 +313,10 @@ def norm_backward(z, h, dz, dy, *, gate=None, post_weight=None, weight=None, bia
         names = [n for n in _NORM_GRADS if have[n] is not None] if wants is None else wants
         for n in names:
             _need(n in _NORM_GRADS, f"no gradient {n!r}")
-        p = _norm_plan(key, z, h, gate, post_weight, weight, bias, scale, None, norm, post_norm, eps, res_scale,
+        p = _norm_plan(z, h, gate, post_weight, weight, bias, scale, None, norm, post_norm, eps, res_scale,
                        rows_per_group, branch, (("dz", "dz", dz, z.dtype), ("dy", "dy", dy, branch)))
         p.a, p.c = branch, ([n for n in _NORM_GRADS[:3] if n in names], [n for n in _NORM_GRADS[3:] if n in names])
+        _keep(key, p)
     if p.copy:
         vecs = [None if v is None else v.contiguous() for v in (post_weight, weight, bias)]
         z, h, dz, dy, gate, scale = (_dense(t) for t in (z, h, dz, dy, gate, scale))
@@ -357,6 +360,7 @@ class _NormFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, *grads):
+        _refuse_capture("block.norm's backward", "norm_backward")
         z, h, gate, post_weight, weight, bias, scale = ctx.saved_tensors
         dz, dy = grads if h is not None else (None, grads[0])
         if dz is None and dy is None:
@@ -431,7 +435,7 @@ def _on16(*tensors):
     return m % 16 == 0
 
 
-def _rotate_plan(key, ins, outs, table, grid, axes, weights, norm, eps, pairs):
+def _rotate_plan(ins, outs, table, grid, axes, weights, norm, eps, pairs):
     """ins, outs: pairs of tensors (Q's, K's) by descriptor fields, the first of ins deciding the shapes."""
     _need(pairs in _PAIRS, f"pairs is 'interleaved' or 'half', not {pairs!r}")
     _need(len(grid) == 3 and len(axes) == 3, "grid and axes have three entries: (T, H, W)")
@@ -465,7 +469,7 @@ def _rotate_plan(key, ins, outs, table, grid, axes, weights, norm, eps, pairs):
                         int(bool(norm)), eps, *(lds.get(f, 0) for f in ("q", "k", "qo", "ko", "dq", "dk")))
     p = _Plan(desc, first.device, copy)
     p.ws_bytes = _abi.head_rotate_ws_bytes(desc)
-    return _keep(key, p)
+    return p
 
 
 def rotate_forward(Q, K, table, *, grid, axes, q_weight=None, k_weight=None, norm=True, eps=1e-6, pairs="interleaved",
@@ -487,8 +491,9 @@ def rotate_forward(Q, K, table, *, grid, axes, q_weight=None, k_weight=None, nor
         for o in (oq, ok):
             _need(o is None or (o.dim() == 3 and _head_stride(o) is not None),
                   "out's heads must lie densely on 16-byte boundaries")
-        p = _rotate_plan(key, ((("q", "k"), (Q, K)),), ((("qo", "ko"), (oq, ok)),), table, grid, axes,
+        p = _rotate_plan(((("q", "k"), (Q, K)),), ((("qo", "ko"), (oq, ok)),), table, grid, axes,
                          (q_weight, k_weight), norm, eps, pairs)
+        _keep(key, p)
     if p.copy or not _on16(Q, K, table, q_weight, k_weight):
         vecs = [None if v is None else v.clone(memory_format=torch.contiguous_format) for v in (q_weight, k_weight)]
         _need(_on16(oq, ok), "out must lie on 16-byte boundaries")
@@ -535,9 +540,10 @@ def rotate_backward(Q, K, dQr, dKr, table, *, grid, axes, q_weight=None, k_weigh
         for n in names:
             _need(n in ("dq_weight", "dk_weight") and norm and (dQr if n == "dq_weight" else dKr) is not None,
                   f"no gradient {n!r} here")
-        p = _rotate_plan(key, ((("dq", "dk"), (dQr, dKr)), (("q", "k"), (Q, K))), (), table, grid, axes,
+        p = _rotate_plan(((("dq", "dk"), (dQr, dKr)), (("q", "k"), (Q, K))), (), table, grid, axes,
                          (q_weight, k_weight), norm, eps, pairs)
         p.a = names
+        _keep(key, p)
     if p.copy or not _on16(Q, K, dQr, dKr, table, q_weight, k_weight):
         vecs = [None if v is None else v.clone(memory_format=torch.contiguous_format) for v in (q_weight, k_weight)]
         return rotate_backward(_aligned(Q), _aligned(K), _aligned(dQr), _aligned(dKr),
@@ -577,6 +583,7 @@ class _RotateFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dQr, dKr):
+        _refuse_capture("block.rotate's backward", "rotate_backward")
         Q, K, wq, wk, table = ctx.saved_tensors
         if dQr is None and dKr is None:
             return (None,) * 6
@@ -694,8 +701,9 @@ def expert_dispatch(x, plan, *, out=None):
         ld = _by_token(x, plan, None, None, "x")
         _sorted(out, plan, x.shape[1], x.dtype, "out")
         _need(out is None or out.is_contiguous(), "out must be dense")
-        p = _keep(key, _Plan(call.desc, plan.device, ld is None))
+        p = _Plan(call.desc, plan.device, ld is None)
         p.a = (_DT[x.dtype], x.shape[1], ld, _extent(x), _extent(out))
+        _keep(key, p)
     if p.copy:
         return expert_dispatch(x.contiguous(), plan, out=out)
     if not _current(p.index):
@@ -728,9 +736,10 @@ def expert_combine(ys, plan, weights=None, *, add=None, out=None):
         C = ys.shape[1]
         ld_add, ld_out = _by_token(add, plan, C, ys.dtype, "add"), _by_token(out, plan, C, ys.dtype, "out")
         _need(ld_out is not None, "out's rows must lie evenly")
-        p = _keep(key, _Plan(call.desc, plan.device, ld_add is None or not ys.is_contiguous()
-                             or (weights is not None and not weights.is_contiguous())))
+        p = _Plan(call.desc, plan.device, ld_add is None or not ys.is_contiguous()
+                  or (weights is not None and not weights.is_contiguous()))
         p.a = (_DT[ys.dtype], C, ld_add, ld_out)
+        _keep(key, p)
     if p.copy:
         return expert_combine(ys.contiguous(), plan, None if weights is None else weights.contiguous(),
                               add=_dense(add), out=out)
@@ -768,9 +777,10 @@ def expert_combine_backward(dout, ys, plan, weights=None, *, out=None, want_weig
         _sorted(ys, plan, C, dout.dtype, "ys")
         _sorted(out, plan, C, dout.dtype, "out")
         _need(out is None or out.is_contiguous(), "out must be dense")
-        p = _keep(key, _Plan(call.desc, plan.device, ld is None or (ys is not None and not ys.is_contiguous())
-                             or (weights is not None and not weights.is_contiguous())))
+        p = _Plan(call.desc, plan.device, ld is None or (ys is not None and not ys.is_contiguous())
+                  or (weights is not None and not weights.is_contiguous()))
         p.a = (_DT[dout.dtype], C, ld, _extent(out), _extent(ys), _extent(dout), _extent(weights))
+        _keep(key, p)
     if p.copy:
         return expert_combine_backward(_dense(dout), None if ys is None else ys.contiguous(), plan,
                                        None if weights is None else weights.contiguous(), out=out,
@@ -813,6 +823,7 @@ class _DispatchFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dxs):
+        _refuse_capture("block.dispatch's backward", "expert_combine")
         return expert_combine(dxs, ctx.plan), None
 
 
@@ -827,6 +838,7 @@ class _CombineFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
+        _refuse_capture("block.combine's backward", "expert_combine_backward")
         ys, weights = ctx.saved_tensors
         need = ctx.needs_input_grad
         dys = dw = None

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
         s.h0 += HU * stride;
         if (s.h0 >= sd.heads) begin(s, s.it + warps);
     };
-    // lanes past the last head repeat it; they neither store nor add to dw
+    // Lanes past the last head repeat it (or, where the results take its place, them); they neither store nor add to dw.
     auto head_of = [&](const Step& s, int u) {
         const int h = s.h0 + sub + u * stride;
         return h < sd.heads ? h : sd.heads - 1;
@@ -307,11 +307,13 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
                     float q = sum(q2), m = sum(m2);
                     lanes_sum<LPH>(q, m, l);
                     const float r = rsqrtf(q * (1.f / D) + a.eps);
-                    const F2 r2 = f2(r), rd = f2(in ? r : 0.f), k = f2(-(r * r) * (r * m) * (1.f / D));
+                    const F2 r2 = f2(r), k = f2(-(r * r) * (r * m) * (1.f / D));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        dw.a[i] = fma(t.a[i], rd, dw.a[i]);
-                        dw.b[i] = fma(t.b[i], rd, dw.b[i]);
+                        if (in) {
+                            dw.a[i] = fma(t.a[i], r2, dw.a[i]);
+                            dw.b[i] = fma(t.b[i], r2, dw.b[i]);
+                        }
                         o.a[i] = fma(v.a[i], k, o.a[i] * w.a[i] * r2);
                         o.b[i] = fma(v.b[i], k, o.b[i] * w.b[i] * r2);
                     }

@@ -6,6 +6,8 @@ most 8 sums in a thread, 5 in a warp and 5 over the warps of each of up to four 
 moment, both again of the branch) and about twenty products, so K = 128 covers them; a sum over n rows adds
 at most n.  All but a few terms stay far below that.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -340,6 +342,8 @@ ROT_CASES = [
     (90, (2, 5, 9), (0, 32, 0), 33, 0, 64, BF16, "half", False),
     (90, (2, 5, 9), (0, 0, 0), 0, 4, 128, F32, "interleaved", False),
     (5000, (8, 25, 25), (22, 21, 21), 2, 3, 128, F32, "half", True),
+    (333, (1, 9, 37), (10, 30, 20), 0, 3, 128, BF16, "interleaved", True),
+    (3000, (2, 30, 50), (10, 11, 11), 0, 5, 64, F32, "half", True),
 ]
 
 
@@ -744,6 +748,88 @@ def test_differentiable_forms_refuse_capture():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, block.norm_forward(x.detach())[1])
+
+
+def test_a_captured_backward_of_an_eager_graph_is_refused():
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        x = gen(54)(16, 64).requires_grad_()
+        y = block.norm(x, norm="rms")[1]
+        one = torch.ones_like(y)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        g.capture_begin()
+        try:
+            with pytest.raises(RuntimeError, match="captured"):
+                y.backward(one)
+        finally:
+            g.capture_end()
+    torch.cuda.synchronize()
+    assert x.grad is None
+
+
+def test_calls_from_two_threads():
+    """Two threads, a stream each, calls of many signatures for the first time."""
+    import threading
+    n = gen(55)
+    cases = [(n(r, c), n(r, c), n(r, c)) for r in (3, 17, 64) for c in (32, 100, 513, 2048)]
+    want = [(block.norm_forward(x, h, norm="rms", eps=2e-6), block.norm_backward(x, h, x, dy, norm="rms", eps=2e-6))
+            for x, h, dy in cases]
+    torch.cuda.synchronize()
+    block._plans.clear()
+    bad, streams = [], [torch.cuda.Stream() for _ in range(2)]
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for _ in range(20):
+                    for (x, h, dy), (f, g) in zip(cases, want):
+                        z, y = block.norm_forward(x, h, norm="rms", eps=2e-6)
+                        b = block.norm_backward(x, h, x, dy, norm="rms", eps=2e-6)
+                        if not (torch.equal(z, f[0]) and torch.equal(y, f[1]) and torch.equal(b["dh"], g["dh"])):
+                            bad.append(tuple(x.shape))
+        except Exception as e:                  # to be seen by the test, not lost with the thread
+            bad.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_results_in_place_of_inputs_through_the_library():
+    """The overlaps that include/prism.h allows give the bits of separate outputs."""
+    n = gen(56)
+    L = _abi.lib()
+    st = torch.cuda.current_stream().cuda_stream
+    for R, C in ((70, 2048), (70, 96), (40, 5120)):
+        for norm in ("layer", "rms"):
+            z, h, dz, dy = (n(R, C, dt=BF16) for _ in range(4))
+            g = block.norm_backward(z, h, dz, dy, norm=norm, post_norm="rms")
+            d = _abi.BlockNormT(R, R, C, 1, 1, {"rms": 1, "layer": 2}[norm], 1, 1e-6, 1.0)
+            assert L.prism_block_norm_bwd(ctypes.addressof(d), z.data_ptr(), h.data_ptr(), None, None, None, None, None,
+                                          dz.data_ptr(), dy.data_ptr(), dz.data_ptr(), h.data_ptr(), None, None, None,
+                                          None, None, None, None, 0, st) == 0
+            assert torch.equal(dz, g["dx"]) and torch.equal(h, g["dh"])
+    grid, axes = (1, 8, 8), (10, 11, 11)
+    table = block.rotation_table(grid, axes)
+    for dt, pairs in ((BF16, 0), (BF16, 1), (F32, 0)):
+        Q, dr, w = n(64, 3, 64, dt=dt), n(64, 3, 64, dt=dt), 1 + n(64, std=0.2)
+        g = block.rotate_backward(Q, None, dr, None, table, grid=grid, axes=axes, q_weight=w,
+                                  pairs=("interleaved", "half")[pairs])
+        d = _abi.RotateT(64, *grid, 3, 0, 64, *axes, pairs, int(dt == BF16), 1, 1e-6)
+        ws = torch.empty(_abi.head_rotate_ws_bytes(d), dtype=torch.uint8, device="cuda")
+        dw = torch.empty(64, device="cuda")
+        assert L.prism_head_rotate_bwd(ctypes.addressof(d), Q.data_ptr(), None, w.data_ptr(), None, table.data_ptr(),
+                                       dr.data_ptr(), None, dr.data_ptr(), None, dw.data_ptr(), None, ws.data_ptr(),
+                                       ws.numel(), st) == 0
+        assert torch.equal(dr, g["dQ"]) and torch.equal(dw, g["dq_weight"])
+    ids = routed(n, 50, 2, 6, 0.1)
+    plan = block.expert_plan(ids, 6)
+    ys, add = n(plan.rows_sorted, 40), n(50, 40)
+    want = block.expert_combine(ys, plan, add=add)
+    assert block.expert_combine(ys, plan, add=add, out=add) is add and torch.equal(add, want)
 
 
 def test_launches_are_counted():
