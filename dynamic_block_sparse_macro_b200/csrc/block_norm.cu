@@ -149,7 +149,7 @@ static Split split_rows(const prism_block_norm_t* n, bool one_group) {
     if (n->rows == 0) return s;
     s.rpg = !one_group && n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
     s.groups = (n->rows + s.rpg - 1) / s.rpg;
-    const int64_t teams = (int64_t)kSMs * sm_teams(n->channels, bwd_ctas(team_bucket(team_threads(n->channels))));
+    const int64_t teams = (int64_t)kSMs * sm_teams(n->channels, bwd_ctas(team_bucket(team_threads(n->channels)), n->branch_dtype == PRISM_F32));
     const int64_t per_cta = cta_teams(n->channels), ctas = teams / per_cta;
     // of the CTAs a group's share by its rows: the last group may be shorter than the others
     int64_t per = (s.groups * 4 <= ctas ? ctas : 8 * ctas) * s.rpg / n->rows;

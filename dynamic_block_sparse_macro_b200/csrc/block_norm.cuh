@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fw
     if constexpr (RING) cp_wait<0>();
 }
 
-constexpr bool vec_shared(int maxt) { return maxt > 640; }
+constexpr bool vec_shared(int maxt, bool f32) { return maxt > 640 || (maxt == 384 && !f32); }
 constexpr int kTeamSums = 256 * 8 * 3 * (int)sizeof(float);       // of the teams of a CTA that are each within a warp
 
 // What the backward's branch is: none, one that goes to the sum as it is, or one with a norm of its own.
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_bw
 
     // The vectors stay in registers, or where these are too few (the widest teams) in shared memory behind the
     // ring, read again for each use.
-    constexpr bool VSM = vec_shared(MAXT);
+    constexpr bool VSM = vec_shared(MAXT, sizeof(TX) + sizeof(TH) == 8);
     const uint32_t vec = (uint32_t)__cvta_generic_to_shared(g_ring) + (RING ? D * stage_bytes : 0) + tid * 16;
     auto keep = [&](const F2 (&v)[4], int which) {
 #pragma unroll
@@ -884,14 +884,14 @@ inline int cta_teams(int C) {
 }
 // the kernel's MAXT for a team, and the CTAs of at most that many threads that its registers leave room for on an SM
 constexpr int team_bucket(int threads) {
-    return threads <= 32 ? 32 : threads <= 256 ? 256 : threads <= 384 ? 384 : threads <= 512 ? 512 : threads <= 640 ? 640 : threads <= 768 ? 768 : 1024;
+    return threads <= 32 ? 32 : threads <= 256 ? 256 : threads <= 320 ? 320 : threads <= 384 ? 384 : threads <= 512 ? 512 : threads <= 640 ? 640 : threads <= 768 ? 768 : 1024;
 }
 constexpr int fwd_ctas(int maxt, int unit, bool branch) {
     if (maxt <= 256) return maxt == 32 || unit < 4 ? 2 : 3;
     if (!branch && unit >= 4) return maxt <= 384 ? 3 : maxt <= 768 ? 2 : 1;
-    return maxt <= 384 ? 2 : 1;
+    return maxt <= 384 || (unit >= 4 && maxt <= 512) ? 2 : 1;
 }
-constexpr int bwd_ctas(int maxt) { return maxt <= 256 ? 2 : 1; }
+constexpr int bwd_ctas(int maxt, bool f32) { return maxt <= 320 || (maxt <= 384 && !f32) ? 2 : 1; }    // f32: stream and branch
 // teams that run at a time on an SM
 inline int sm_teams(int C, int ctas) {
     const int t = team_threads(C), most = team_bucket(t) == 32 ? 256 : team_bucket(t);
@@ -902,8 +902,9 @@ inline int sm_teams(int C, int ctas) {
 constexpr int kRowsAhead = 3;
 template <typename TX, typename TH, int E, int MAXT, int H>
 prism_status_t launch_bwd_one(const BwdArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
-    constexpr int CTAS = bwd_ctas(MAXT), row = 8 * (int)(2 * sizeof(TX) + (H ? 2 : 1) * sizeof(TH));
-    constexpr int threads = MAXT == 32 ? 256 : MAXT, vec = vec_shared(MAXT) ? (H ? 64 : 32) : 0;
+    constexpr bool f32 = sizeof(TX) + sizeof(TH) == 8;
+    constexpr int CTAS = bwd_ctas(MAXT, f32), row = 8 * (int)(2 * sizeof(TX) + (H ? 2 : 1) * sizeof(TH));
+    constexpr int threads = MAXT == 32 ? 256 : MAXT, vec = vec_shared(MAXT, f32) ? (H ? 64 : 32) : 0;
     constexpr int most = ((216 << 10) / CTAS - vec * threads) / (row * threads);
     constexpr int D = most < 1 ? 1 : most > kRowsAhead ? kRowsAhead : most;
     auto kernel = &k_block_norm_bwd<TX, TH, E, MAXT, H, CTAS, D>;
@@ -936,6 +937,7 @@ template <typename TX, typename TH> prism_status_t launch_bwd(const BwdArgs& a, 
     switch (team_bucket(block.x)) {                                                   \
         case 32: return ONE<TX, TH, E, 32, H>(a, grid, block, s);                     \
         case 256: return ONE<TX, TH, E, 256, H>(a, grid, block, s);                   \
+        case 320: return ONE<TX, TH, E, 320, H>(a, grid, block, s);                   \
         case 384: return ONE<TX, TH, E, 384, H>(a, grid, block, s);                   \
         case 512: return ONE<TX, TH, E, 512, H>(a, grid, block, s);                   \
         case 640: return ONE<TX, TH, E, 640, H>(a, grid, block, s);                   \
