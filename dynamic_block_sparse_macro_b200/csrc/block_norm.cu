@@ -24,10 +24,9 @@ struct JoinArgs {
 };
 
 // The segments' column sums to the vectors' gradients.  32 channels a CTA, whose 16 warps take every 16th segment.
-// The CTAs of a cluster share the work out among them: the segments of each group in turn where groups are few and
-// long (`wide`), the segments where each has whole groups, else the groups; the first of them adds up what the others
-// have.  All in a
-// fixed order, so that the result does not depend on scheduling.
+// The CTAs of a cluster share the work out among them: the segments where there is one group and a long one (`wide`)
+// or each segment has whole groups, else the groups; the first of them adds up what the others have.  All in a fixed
+// order, so that the result does not depend on scheduling.
 constexpr int kJoinRows = 16, kMaxCluster = 8;
 __global__ void __launch_bounds__(32 * kJoinRows) k_block_norm_join(const JoinArgs a) {
     __shared__ float sh[kJoinRows][3][32];
@@ -106,12 +105,9 @@ __global__ void __launch_bounds__(32 * kJoinRows) k_block_norm_join(const JoinAr
         read(a.segs * me / n, a.segs * (me + 1) / n, t);
         gather(t);
     } else if (a.wide) {
-        for (int64_t g = 0; g < a.groups; ++g) {
-            const int64_t s0 = g * a.per_group;
-            read(s0 + a.per_group * me / n, s0 + a.per_group * (me + 1) / n, v);
-            gather(v);
-            if (me == 0 && y == 0 && in) group(g, v);
-        }
+        read(a.per_group * me / n, a.per_group * (me + 1) / n, v);
+        gather(v);
+        if (me == 0 && y == 0 && in) group(0, v);
     } else {
         for (int64_t g = me; g < a.groups; g += n) {
             read(g * a.per_group, (g + 1) * a.per_group, v);
@@ -126,13 +122,13 @@ __global__ void __launch_bounds__(32 * kJoinRows) k_block_norm_join(const JoinAr
 }
 
 static prism_status_t launch_join(JoinArgs j, cudaStream_t stream) {
-    // one group of 148 segments: 6 us by one CTA a column, 12 by a cluster; of 9472: 75 against 15
-    j.wide = j.groups <= 4 && j.per_group >= 512;
+    // one group of 1184 segments: 6 us by a cluster, 11 by one CTA a column; of 148: 12 and 6; two of 592: 8 and 7
+    j.wide = j.groups == 1 && j.per_group >= 512;
     const int64_t parts = j.per_group == 0 || j.wide ? kMaxCluster : j.groups;
     int n = 1;
     while (n < kMaxCluster && 2 * n <= parts) n *= 2;
-    return launch_after(k_block_norm_join, dim3((unsigned)((j.C + 31) / 32), (unsigned)n), dim3(32, kJoinRows), n, stream, j)
-               ? PRISM_OK : PRISM_ERR_CUDA;
+    const dim3 grid((unsigned)((j.C + 31) / 32), (unsigned)n);
+    return launch_after(k_block_norm_join, grid, dim3(32, kJoinRows), n, stream, j) ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
 struct Split {
@@ -140,16 +136,17 @@ struct Split {
     int per_group;               // segments a group; 0: a segment has whole groups
 };
 
-// Segments of rows.  Where there are few groups, each is cut so that the segments fill the teams that run at a time
-// once; where groups are many, into about eight rounds of such teams, so that the last round's idle part is small.
-// No segment below four rows (two where teams are left over) is cut: its column sums cost as much as three rows.  Groups that are not cut are shared
-// out in runs among the teams.
+// Segments of rows, one a CTA.  Where there are few groups, each is cut so that the segments fill the CTAs that run at
+// a time once; where groups are many, into about eight rounds of such CTAs, so that the last round's idle part is
+// small.  A segment has four rows a team at least (two where CTAs are left over): its column sums cost as much as three.
+// Groups that are not cut are shared out among the teams in runs.
 static Split split_rows(const prism_block_norm_t* n, bool one_group) {
     Split s{0, 1, 0, 0};
     if (n->rows == 0) return s;
     s.rpg = !one_group && n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
     s.groups = (n->rows + s.rpg - 1) / s.rpg;
-    const int64_t teams = (int64_t)kSMs * sm_teams(n->channels, bwd_ctas(team_bucket(team_threads(n->channels)), n->branch_dtype == PRISM_F32));
+    const int ctas_sm = bwd_ctas(team_bucket(team_threads(n->channels)), n->branch_dtype == PRISM_F32);
+    const int64_t teams = (int64_t)kSMs * sm_teams(n->channels, ctas_sm);
     const int64_t per_cta = cta_teams(n->channels), ctas = teams / per_cta;
     // of the CTAs a group's share by its rows: the last group may be shorter than the others
     int64_t per = (s.groups * 4 <= ctas ? ctas : 8 * ctas) * s.rpg / n->rows;
@@ -237,8 +234,9 @@ extern "C" prism_status_t prism_block_norm_fwd(const prism_block_norm_t* n, cons
     a.R = n->rows;
     a.rpg = n->rows_per_group < n->rows ? n->rows_per_group : n->rows;
     a.C = C; a.norm = n->norm; a.post = n->post_norm; a.eps = n->eps; a.res = n->res_scale;
-    const int unit = unit_of(eb == 2 ? 8 : 4, C, {a.ld_x, h ? a.ld_h : 0, h ? a.ld_z : 0, has_y ? a.ld_y : 0, gate ? a.ld_gate : 0,
-                                 scale ? a.ld_scale : 0, shift ? a.ld_shift : 0},
+    const int unit = unit_of(eb == 2 ? 8 : 4, C,
+                             {a.ld_x, h ? a.ld_h : 0, h ? a.ld_z : 0, has_y ? a.ld_y : 0, gate ? a.ld_gate : 0,
+                              scale ? a.ld_scale : 0, shift ? a.ld_shift : 0},
                              {x, h, gate, w_post, w, b, scale, shift, z, y});
     if (n->stream_dtype == PRISM_BF16) st = launch_fwd<__nv_bfloat16, __nv_bfloat16>(a, unit, stream);
     else if (n->branch_dtype == PRISM_BF16) st = launch_fwd<float, __nv_bfloat16>(a, unit, stream);
@@ -293,8 +291,9 @@ extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, cons
     a.R = n->rows;
     a.rpg = s.rpg; a.groups = s.groups; a.segs = s.segs; a.per_group = s.per_group;
     a.C = C; a.norm = n->norm; a.post = n->post_norm; a.eps = n->eps; a.res = n->res_scale;
-    const int unit = unit_of(es == 2 ? 8 : 4, C, {has_y ? a.ld_z : 0, h ? a.ld_h : 0, dz ? a.ld_dz : 0, has_y ? a.ld_dy : 0, a.ld_dx,
-                                 h ? a.ld_dh : 0, gate ? a.ld_gate : 0, scale ? a.ld_scale : 0},
+    const int unit = unit_of(es == 2 ? 8 : 4, C,
+                             {has_y ? a.ld_z : 0, h ? a.ld_h : 0, dz ? a.ld_dz : 0, has_y ? a.ld_dy : 0, a.ld_dx,
+                              h ? a.ld_dh : 0, gate ? a.ld_gate : 0, scale ? a.ld_scale : 0},
                              {has_y ? z : nullptr, h, gate, w_post, w, b, scale, dz, dy, dx, dh, dgate, dscale, dshift,
                               part ? ws : nullptr});
     if (n->stream_dtype == PRISM_BF16) st = launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, unit, stream);

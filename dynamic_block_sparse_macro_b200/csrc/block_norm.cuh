@@ -23,13 +23,13 @@
 //     at the measured copy rate); with more CTAs an SM (64 registers, 112 bytes) 747;
 //   - fp32 pairs in one instruction: the backward of 61440 x 2048 339 -> 248 us, rows copied three ahead included; with
 //     one barrier a row less 243 (233);
-//   - teams of more than 256 threads have an SM to themselves and leave it idle at each of a row's barriers: 8191 x 5120
-//     with two rms norms 98 us (78), 13269 x 8192 276 (202).  Clusters of CTAs of 256 threads in their place wait longer
-//     for one another: 13269 x 4096 149 us instead of 128, with the cluster's own barrier 229.
+//   - the widest teams (more than 512 threads, backwards 384) have an SM to themselves and leave it idle at each of a
+//     row's barriers: 8191 x 5120 with two rms norms 98 us (78), 13269 x 8192 276 (202).  Clusters of CTAs of 256 threads
+//     in their place wait longer for one another: 13269 x 4096 149 us instead of 128, with the cluster's barrier 229.
 //   - rows of odd width move element by element: 40000 x 1001 bf16 218 us backwards, x 1000 93.
 #pragma once
 
-#include <type_traits>
+#include <initializer_list>
 
 #include "rows.cuh"
 
@@ -882,9 +882,14 @@ inline int cta_teams(int C) {
     const int t = team_threads(C);
     return t <= 32 ? 256 / t : 1;
 }
-// the kernel's MAXT for a team, and the CTAs of at most that many threads that its registers leave room for on an SM
+// The kernel's MAXT for a team, and the CTAs of that many threads that an SM takes: as many as the registers allow
+// without spills, or with few.  Forward: 2048 channels three CTAs 501 us, two 571, four with 32 bytes of spills 597
+// (131072 rows); 4096 two 75, one 85 (13269 rows); 5416 without a branch two 72, one 91.  Backward: 2048 two 361 and
+// three with 32 bytes 421 (61440 rows, before the pairs of fp32); 2560 two 72, one 92 (13269 rows).
 constexpr int team_bucket(int threads) {
-    return threads <= 32 ? 32 : threads <= 256 ? 256 : threads <= 320 ? 320 : threads <= 384 ? 384 : threads <= 512 ? 512 : threads <= 640 ? 640 : threads <= 768 ? 768 : 1024;
+    for (int b : {32, 256, 320, 384, 512, 640, 768})
+        if (threads <= b) return b;
+    return 1024;
 }
 constexpr int fwd_ctas(int maxt, int unit, bool branch) {
     if (maxt <= 256) return maxt == 32 || unit < 4 ? 2 : 3;

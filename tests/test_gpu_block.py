@@ -80,6 +80,7 @@ NORM_CASES = [
     (5000, 520, 1000, BF16, BF16, "layer", "rms", ALL, 1.0),
     (20000, 40, 700, F32, F32, "rms", "layer", ALL, 1.0),
     (40000, 96, 40000, BF16, BF16, "layer", "rms", ALL, 1.0),
+    (6001, 320, 6001, BF16, BF16, "layer", "rms", ALL, 1.0),
 ]
 
 
