@@ -162,12 +162,14 @@ template <typename T, bool HALF> struct Copy {
 
 // CTAs on an SM, heads of a lane at a time and steps that are copied ahead (0: a step's rows are loaded when it begins):
 // what the registers allow without spills, at 24 heads of 128 channels.
-// Forward: bf16 5 x 2 1150 us, 3 x 4 1182, 4 x 4 1206 (294912 tokens); f32 3 x 4 251-271, 5 x 2 266-295 (30720).
+// Forward (294912 tokens, passes back to back): bf16 4 x 3 1167 us, 3 x 6 1172, 3 x 4 1192, 4 x 4 1211, 5 x 3 with 24
+// bytes of spills 1247, 4 x 2 1286, 3 x 3 1308; f32 (30720)
+// 3 x 2 246, 3 x 3 249-263, 3 x 4 249-271.
 // Backward (61440 tokens, bf16): interleaved 3 x 1, 4 ahead 364 us, 3 x 2, 2 ahead 402, without copies 401; half
 // 3 x 2, 2 ahead 358, 3 x 1, 4 ahead 380.  f32 (30720): 2 x 2 without copies 355; a lane's eight floats are two
 // copies that leave gaps in a warp's access: interleaved 585.
-constexpr int ctas_sm(int elem, bool bwd) { return bwd ? (elem == 2 ? 3 : 2) : elem == 2 ? 5 : 3; }
-constexpr int heads_at_once(int elem, bool half, bool bwd) { return bwd ? (elem == 2 && !half ? 1 : 2) : elem == 2 ? 2 : 4; }
+constexpr int ctas_sm(int elem, bool bwd) { return bwd ? (elem == 2 ? 3 : 2) : elem == 2 ? 4 : 3; }
+constexpr int heads_at_once(int elem, bool half, bool bwd) { return bwd ? (elem == 2 && !half ? 1 : 2) : elem == 2 ? 3 : 2; }
 constexpr int steps_ahead(int elem, bool half, bool bwd) { return bwd && elem == 2 ? (half ? 2 : 4) : 0; }
 extern __shared__ __align__(16) char g_rows[];
 
@@ -215,6 +217,7 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
         return h < sd.heads ? h : sd.heads - 1;
     };
     Step now, ahead;
+    auto none = [&](int u) { return u && now.h0 + u * stride >= sd.heads; };     // no lane of the warp has a u-th head
     begin(now, (int64_t)blockIdx.x * 8 + warp);
     ahead = now;
     const uint32_t ring = S ? (uint32_t)__cvta_generic_to_shared(g_rows) + threadIdx.x * CP::B : 0u;
@@ -238,6 +241,7 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
         for (int i = 0; i < S; ++i) fetch(i);
     }
     F2 cs[2], sn[2], sm[2];                      // sm = -sn
+    F2 ta[2], tb[2], ua[2], ub[2];               // forward: the turn with the weights in it, a' = a ta + b tb, b' = a ua + b ub
     // every lane of the warp takes part in the exchanges of every step
     while (now.it < items) {
         Raw<T, HALF> px[HU], pr[BWD ? HU : 1];
@@ -257,28 +261,39 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
             angles(a, now.token, l, cs, sn);
             sm[0] = sn[0] * f2(-1.f);
             sm[1] = sn[1] * f2(-1.f);
+            if constexpr (!BWD) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ta[i] = w.a[i] * cs[i];
+                    tb[i] = w.b[i] * sm[i];
+                    ua[i] = w.a[i] * sn[i];
+                    ub[i] = w.b[i] * cs[i];
+                }
+            }
         }
         T* out = (T*)sd.out + (int64_t)now.token * sd.ld_out + c0;
 #pragma unroll
         for (int u = 0; u < HU; ++u) {
+            // Not so around the loads, which go out together: 16 heads bf16 (61440 tokens) 181 us, with it there 185, without 188.
+            if (S == 0 && none(u)) break;
             const bool in = now.h0 + sub + u * stride < sd.heads;
             Pairs v, o;
             if constexpr (!BWD) {
                 v = pairs_of<T, HALF>(px[u]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    o.a[i] = fma(v.a[i], ta[i], v.b[i] * tb[i]);
+                    o.b[i] = fma(v.a[i], ua[i], v.b[i] * ub[i]);
+                }
                 if (a.norm) {
                     const float q = lanes_sum<LPH>(sum(fma(v.a[0], v.a[0], v.a[1] * v.a[1]) +
                                                        fma(v.b[0], v.b[0], v.b[1] * v.b[1])));
                     const F2 r = f2(rsqrtf(q * (1.f / D) + a.eps));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        v.a[i] = v.a[i] * (r * w.a[i]);
-                        v.b[i] = v.b[i] * (r * w.b[i]);
+                        o.a[i] = o.a[i] * r;
+                        o.b[i] = o.b[i] * r;
                     }
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    o.a[i] = fma(v.a[i], cs[i], v.b[i] * sm[i]);
-                    o.b[i] = fma(v.a[i], sn[i], v.b[i] * cs[i]);
                 }
             } else {
                 const char* row = g_rows + stage * kStage + 2 * u * kRow + threadIdx.x * CP::B;
@@ -368,7 +383,7 @@ __global__ void __launch_bounds__(512) k_head_rotate_join(const float* part, int
     }
 }
 
-constexpr int kMaxCtas = kSMs * 5;     // as many as run at a time
+constexpr int kMaxCtas = kSMs * 4;     // as many as run at a time
 
 static prism_status_t check(const prism_rotate_t* p) {
     if (!p) return PRISM_ERR_INVALID_ARG;
