@@ -388,7 +388,8 @@ constexpr int kMaxCtas = kSMs * 4;     // as many as run at a time
 static prism_status_t check(const prism_rotate_t* p) {
     if (!p) return PRISM_ERR_INVALID_ARG;
     if (p->tokens < 0 || p->T < 1 || p->H < 1 || p->W < 1) return PRISM_ERR_SHAPE;
-    if (p->tokens > INT32_MAX || (int64_t)p->T * p->H * p->W > INT32_MAX ||
+    // one factor at a time: the product of three may pass 64 bits
+    if (p->tokens > INT32_MAX || (int64_t)p->T * p->H > INT32_MAX || (int64_t)p->T * p->H * p->W > INT32_MAX ||
         (int64_t)p->T * p->pairs_t + (int64_t)p->H * p->pairs_h + (int64_t)p->W * p->pairs_w > INT32_MAX)
         return PRISM_ERR_UNSUPPORTED;
     if (p->dtype != PRISM_F32 && p->dtype != PRISM_BF16) return PRISM_ERR_UNSUPPORTED;
