@@ -173,8 +173,7 @@ def _check_out(out, what, allowed, *others):
     if allowed is not None and not _apart(out, allowed):
         _need(_itself(out, allowed), f"{what} overlaps an input without being it")
     for t in others:
-        _need(_apart(out, t) or (allowed is not None and _itself(out, allowed) and _itself(t, allowed)),
-              f"{what} overlaps another argument")
+        _need(_apart(out, t), f"{what} overlaps another argument")
 
 
 def _refuse_capture(name, instead):
@@ -274,7 +273,8 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
                                 shift=shift, norm=norm, post_norm=post_norm, eps=eps, res_scale=res_scale,
                                 rows_per_group=rows_per_group, out_dtype=out_dtype, z=z, y=y)
     if z is not None:
-        _check_out(z, "z", x, h, gate, post_weight, weight, bias, scale, shift)
+        # h may be x, in place too: a row's h is read before its z is written
+        _check_out(z, "z", x, None if _itself(h, x) else h, gate, post_weight, weight, bias, scale, shift)
     elif h is not None:
         z = _like(x, x.dtype)
     if y is not None:

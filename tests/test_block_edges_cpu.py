@@ -18,6 +18,52 @@ def L():
     return _abi.lib()
 
 
+@pytest.fixture
+def host(monkeypatch):
+    """The tensor calls on CPU tensors, up to the library: the device check is passed over, and a call that gets
+    through every check raises ``Through``."""
+    class Through(Exception):
+        pass
+
+    def through(index):
+        raise Through
+    monkeypatch.setattr(block, "_same_device", lambda dev, *t: None)
+    monkeypatch.setattr(block, "_stream", through)
+    monkeypatch.setattr(block, "_current", lambda index: True)
+    monkeypatch.setattr(block, "_plans", {})
+    return Through
+
+
+def test_an_output_that_is_also_a_second_input_is_refused(L, host):
+    """With one choice a token and no padding, sorted and token buffers have one shape, and the tensor that an output
+    may take the place of can be another argument too, which other tokens still read."""
+    p = block.ExpertPlan(6, 1, 3, 1, 8, torch.device("cpu"))
+    t, o = torch.zeros(6, 8), torch.zeros(6, 8)
+    assert p.rows_sorted == 6
+    for f in (lambda: block.expert_combine(t, p, add=t, out=t),
+              lambda: block.expert_combine(t, p, torch.zeros(6, 1), add=t, out=t),
+              lambda: block.expert_combine_backward(t, t, p, out=t),
+              lambda: block.expert_dispatch(t, p, out=t)):
+        with pytest.raises(ValueError, match="overlaps"):
+            f()
+    # each alone is allowed, and so is one tensor as both inputs
+    for f in (lambda: block.expert_combine(o, p, add=t, out=t), lambda: block.expert_combine(t, p, add=t, out=o),
+              lambda: block.expert_combine_backward(o, t, p, out=t), lambda: block.expert_combine(t, p, add=t)):
+        with pytest.raises(host):
+            f()
+    # the norms' vectors of a row each: read after the row of z is written
+    x, h = torch.zeros(6, 8), torch.zeros(6, 8)
+    for k in ("scale", "shift", "gate"):
+        with pytest.raises(ValueError, match="overlaps"):
+            block.norm_forward(x, h, z=x, rows_per_group=1, **{k: x})
+    with pytest.raises(ValueError, match="overlaps"):
+        block.norm_forward(x, h, z=h)
+    # the stream itself as the branch, in place or not
+    for z in (None, x, torch.zeros(6, 8)):
+        with pytest.raises(host):
+            block.norm_forward(x, x, z=z)
+
+
 # grids whose number of places passes 64 bits: cut to 64 bits, the products are 0 or below it but for the last
 @pytest.mark.parametrize("grid", [(1 << 16, 1 << 24, 1 << 24), (1 << 24, 1 << 24, 1 << 16), (1 << 21, 1 << 21, 1 << 21),
                                   (1 << 30, 1 << 30, 1 << 4), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1)])
