@@ -903,6 +903,14 @@ inline int sm_teams(int C, int ctas) {
     return ctas * most / t;
 }
 
+// Leave for a kernel's dynamic shared memory, where with the static part it passes the 48 KB that need none.  FULL is
+// what its widest team takes, not the call's: the limit is the kernel's, and a thread with narrower rows may set it
+// between another's setting and its launch.
+template <int FULL, typename F> bool allow_shared(F kernel) {
+    static_assert(FULL <= 224 << 10, "with the static part, what a CTA can have");
+    return FULL <= 40 << 10 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FULL) == cudaSuccess;
+}
+
 // rows ahead in the backward (2: 5% slower, 4: the same), fewer where the widest rows leave no room
 constexpr int kRowsAhead = 3;
 template <typename TX, typename TH, int E, int MAXT, int H>
@@ -913,12 +921,11 @@ prism_status_t launch_bwd_one(const BwdArgs& a, dim3 grid, dim3 block, cudaStrea
     constexpr int most = ((216 << 10) / CTAS - vec * threads) / (row * threads);
     constexpr int D = most < 1 ? 1 : most > kRowsAhead ? kRowsAhead : most;
     auto kernel = &k_block_norm_bwd<TX, TH, E, MAXT, H, CTAS, D>;
-    int bytes = ((Lane<TX, E>::kAsync && Lane<TH, E>::kAsync ? D * row : 0) + vec) * (int)(block.x * block.y);
-    if (MAXT == 32 && bytes < kTeamSums) bytes = kTeamSums;
-    // with the static part, more than the 48 KB that need no leave
-    if (bytes > 40 << 10 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return PRISM_ERR_CUDA;
-    kernel<<<grid, block, bytes, s>>>(a);
+    constexpr int thread = (Lane<TX, E>::kAsync && Lane<TH, E>::kAsync ? D * row : 0) + vec;
+    constexpr int least = MAXT == 32 ? kTeamSums : 0, full = thread * threads > least ? thread * threads : least;
+    if (!allow_shared<full>(kernel)) return PRISM_ERR_CUDA;
+    const int bytes = thread * (int)(block.x * block.y);
+    kernel<<<grid, block, bytes > least ? bytes : least, s>>>(a);
     return PRISM_OK;
 }
 template <typename TX, typename TH, int E, int MAXT, int H>
@@ -927,10 +934,8 @@ prism_status_t launch_fwd_one(const FwdArgs& a, dim3 grid, dim3 block, cudaStrea
     constexpr int row = 8 * (int)(sizeof(TX) + (H != kNoBranch ? sizeof(TH) : 0)), ctas = fwd_ctas(MAXT, E, H != kNoBranch);
     constexpr int most = (216 << 10) / ctas / (row * MAXT), D = !async ? 0 : most > kRowsAhead ? kRowsAhead : most;
     auto kernel = &k_block_norm_fwd<TX, TH, E, MAXT, H != kNoBranch, ctas, D>;
-    const int bytes = D * row * (int)block.x;
-    if (bytes > 40 << 10 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return PRISM_ERR_CUDA;
-    kernel<<<grid, block, bytes, s>>>(a);
+    if (!allow_shared<D * row * MAXT>(kernel)) return PRISM_ERR_CUDA;
+    kernel<<<grid, block, D * row * (int)block.x, s>>>(a);
     return PRISM_OK;
 }
 

@@ -1,0 +1,55 @@
+"""The operators around the attention on the GPU, where a fault would be lost among roundings or needs two callers."""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+from dynamic_block_sparse_macro_b200 import _abi, block
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+# ------------------------------------------------------------------ two callers
+@pytest.mark.parametrize("widths", [(2048, 1024, 1536), (4096, 3200, 4096)])
+def test_threads_in_one_kernel_with_rows_of_other_widths(widths):
+    """Widths that share a kernel but not the size of its shared memory, straight into the library, so that the threads
+    are in it together: every call is accepted, and gives the bits that it gives alone."""
+    g = gen(7)
+    L = _abi.lib()
+    calls = []
+    for C in widths:
+        z, h, dz, dy = (torch.randn(2, C, generator=g, device="cuda") for _ in range(4))
+        d = _abi.BlockNormT(2, 2, C, 0, 0, 2, 0, 1e-6, 1.0)
+        outs = [torch.empty_like(z) for _ in range(4)]
+        want = [*block.norm_forward(z, h), *(block.norm_backward(z, h, dz, dy)[k] for k in ("dx", "dh"))]
+        calls.append((d, z, h, dz, dy, outs, want))
+    torch.cuda.synchronize()
+    codes, go = [set() for _ in widths], threading.Barrier(len(widths))
+    streams = [torch.cuda.Stream() for _ in widths]
+
+    def work(i):
+        d, z, h, dz, dy, outs, _ = calls[i]
+        a, st, p = ctypes.addressof(d), streams[i].cuda_stream, [t.data_ptr() for t in (z, h, dz, dy, *outs)]
+        fwd = (a, p[0], p[1], None, None, None, None, None, None, p[4], p[5], st)
+        bwd = (a, p[0], p[1], None, None, None, None, None, p[2], p[3], p[6], p[7], None, None, None, None, None, None,
+               None, 0, st)
+        go.wait(60)
+        for _ in range(20000):
+            codes[i].add(L.prism_block_norm_fwd(*fwd))
+            codes[i].add(L.prism_block_norm_bwd(*bwd))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(widths))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}] * len(widths)
+    for _, _, _, _, _, outs, want in calls:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
