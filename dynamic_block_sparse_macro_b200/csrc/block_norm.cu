@@ -272,7 +272,7 @@ extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, cons
     if (n->rows == 0) {
         // sums over no rows; there are no groups
         for (float* p : {dw_post, dw, db})
-            if (p && cudaMemsetAsync(p, 0, C * sizeof(float), stream) != cudaSuccess) return PRISM_ERR_CUDA;
+            if (p && !taken(cudaMemsetAsync(p, 0, C * sizeof(float), stream))) return PRISM_ERR_CUDA;
         return PRISM_OK;
     }
     const int es = esize(n->stream_dtype), eb = esize(n->branch_dtype);
@@ -301,6 +301,7 @@ extern "C" prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, cons
     else st = launch_bwd<float, float>(a, unit, stream);
     if (st != PRISM_OK) return st;
     if (!part) return launch_status(1);
+    if (!launched()) return PRISM_ERR_CUDA;           // the join would add up what was never written
     st = launch_join(JoinArgs{(const float*)ws, w, b, w_post, scale, gate, s.per_group ? dgate : nullptr,
                               s.per_group ? dscale : nullptr, s.per_group ? dshift : nullptr, dw, db, dw_post, s.groups,
                               s.segs, a.ld_scale, a.ld_gate, C, s.per_group, 0},

@@ -908,7 +908,7 @@ inline int sm_teams(int C, int ctas) {
 // between another's setting and its launch.
 template <int FULL, typename F> bool allow_shared(F kernel) {
     static_assert(FULL <= 224 << 10, "with the static part, what a CTA can have");
-    return FULL <= 40 << 10 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FULL) == cudaSuccess;
+    return FULL <= 40 << 10 || taken(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FULL));
 }
 
 // rows ahead in the backward (2: 5% slower, 4: the same), fewer where the widest rows leave no room

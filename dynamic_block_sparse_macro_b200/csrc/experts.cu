@@ -551,7 +551,7 @@ extern "C" prism_status_t prism_expert_plan(const prism_experts_t* e, const void
         return launch_status(1);
     }
     k_expert_count<<<(unsigned)ctas, 1024, 0, stream>>>(a);
-    if (!launch_after(k_expert_place, dim3((unsigned)ctas), dim3(1024), 1, stream, a)) return PRISM_ERR_CUDA;
+    if (!launched() || !launch_after(k_expert_place, dim3((unsigned)ctas), dim3(1024), 1, stream, a)) return PRISM_ERR_CUDA;
     return launch_status(2);
 }
 

@@ -493,7 +493,7 @@ static prism_status_t rotate(const prism_rotate_t* p, const void* Q, const void*
     }
     if (p->tokens == 0) {
         for (float* w : {dwq, dwk})
-            if (w && cudaMemsetAsync(w, 0, p->head_dim * sizeof(float), stream) != cudaSuccess) return PRISM_ERR_CUDA;
+            if (w && !taken(cudaMemsetAsync(w, 0, p->head_dim * sizeof(float), stream))) return PRISM_ERR_CUDA;
         return PRISM_OK;
     }
     a.table = (const float2*)table;
@@ -515,7 +515,8 @@ static prism_status_t rotate(const prism_rotate_t* p, const void* Q, const void*
     const prism_status_t r = launch<true>(p, a, grid, stream);
     if (r != PRISM_OK) return r;
     if (dw) {
-        if (!launch_after(k_head_rotate_join, dim3(p->head_dim / 32, sides), dim3(32, 16), 1, stream, (const float*)a.part,
+        if (!launched() ||
+            !launch_after(k_head_rotate_join, dim3(p->head_dim / 32, sides), dim3(32, 16), 1, stream, (const float*)a.part,
                           (int)ctas, (int)p->head_dim, hq ? dwq : dwk, hq ? dwk : (float*)nullptr))
             return PRISM_ERR_CUDA;
     }

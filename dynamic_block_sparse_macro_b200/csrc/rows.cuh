@@ -21,6 +21,11 @@ struct Bits {
 inline bool on(const void* p, int b) { return p != nullptr && (uintptr_t)p % b == 0; }
 inline bool opt_on(const void* p, int b) { return (uintptr_t)p % b == 0; }
 
+// Whether the runtime took the call that has just been made (r: its own answer).  A refusal is this call's to report:
+// nothing further is launched, and it is not left behind for the next call's check.
+inline bool taken(cudaError_t r) { return r == cudaSuccess || (cudaGetLastError(), false); }
+inline bool launched() { return cudaGetLastError() == cudaSuccess; }
+
 // A kernel that finishes another one's work is launched while that one runs and waits for it where it first needs
 // its results, so that its start is not waited for.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -40,7 +45,7 @@ inline bool launch_after(void (*kernel)(A...), dim3 grid, dim3 block, int cluste
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster_y > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+    return taken(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // N consecutive elements of T as they lie in memory

@@ -68,3 +68,51 @@ def test_a_kernels_shared_memory_limit_is_the_same_for_all_its_rows(L):
         assert used[kernel] <= max(n) <= 227 << 10
     for kernel, n in used.items():
         assert n <= 40 << 10 or kernel in limits
+
+
+def calls(L):
+    """One call of each entry point, in the forms that differ in what they launch."""
+    out = {}
+    for C in (64, 2048, 8192):
+        for rows in (0, 1, 5000):
+            n = _abi.BlockNormT(rows, max(1, rows), C, B, B, 2, 0, 1e-6, 1.0)
+            a = ctypes.addressof(n)
+            out["norm", C, rows] = n, lambda a=a: L.prism_block_norm_fwd(a, P, P, None, None, None, None, None, None, P, P,
+                                                                        None)
+            for want in (None, P):
+                out["norm backward", C, rows, want] = n, lambda a=a, want=want: L.prism_block_norm_bwd(
+                    a, P, P, None, None, P, P, None, P, P, P, P, None, None, want, want, None, None, P, 1 << 40, None)
+    for rows in (0, 117):
+        p = _abi.RotateT(rows, 1, 9, 13, 3, 2, 64, 10, 10, 10, 0, B, 1, 1e-6)
+        a = ctypes.addressof(p)
+        out["rotate", rows] = p, lambda a=a: L.prism_head_rotate_fwd(a, P, P, None, None, P, P, P, None)
+        for want in (None, P):
+            out["rotate backward", rows, want] = p, lambda a=a, want=want: L.prism_head_rotate_bwd(
+                a, P, P, None, None, P, P, P, P, P, want, want, P, 1 << 40, None)
+    for rows in (0, 2048, 2049):
+        e = _abi.ExpertsT(rows, 1, 8, 4, 8)
+        a = ctypes.addressof(e)
+        out["plan", rows] = e, lambda a=a: L.prism_expert_plan(a, P, P, P, P, P, P, 1 << 40, None)
+        out["dispatch", rows] = e, lambda a=a: L.prism_expert_dispatch(a, B, 64, P, 0, P, P, P, 1, P, None)
+        out["combine", rows] = e, lambda a=a: L.prism_expert_combine(a, B, 64, P, P, None, None, 0, P, 0, None)
+        out["combine backward", rows] = e, lambda a=a: L.prism_expert_combine_bwd(a, B, 64, P, 0, P, P, None, P, P, 1, P, P,
+                                                                                None)
+    return out
+
+
+def test_a_refused_launch_ends_its_call_and_leaves_no_error(L):
+    """Whichever of a call's steps the runtime refuses, the call reports it, launches nothing more (a sum over what was
+    never written), and the next call's check does not find the error."""
+    seen = set()
+    for name, (_, f) in calls(L).items():
+        L.fake_reset(-1)
+        assert f() == OK, name
+        n = L.fake_count()
+        seen.add((name[0], n))
+        for i in range(n):
+            L.fake_reset(i)
+            assert f() == CUDA, (name, i)
+            assert L.fake_count() == i + 1, (name, i)
+            assert L.fake_last_error() == 0, (name, i)
+    # the forms of more than one step are among them: a limit, a kernel and its join; two memsets; count and placement
+    assert {("norm backward", 3), ("norm backward", 2), ("rotate backward", 2), ("plan", 1), ("plan", 2)} <= seen
