@@ -11,7 +11,8 @@ Each has a differentiable form (``norm``, ``rotate``, ``dispatch``, ``combine``)
 calls it is made of (``*_forward``, ``*_backward``, ``expert_*``), which allocate their outputs and
 workspaces on the current stream, synchronise nothing and may be captured into a CUDA graph.  The
 differentiable forms refuse to run under capture: autograd would tie the captured backward to
-gradient accumulators that may belong to another stream.  Capture the explicit calls instead.
+gradient accumulators that may belong to another stream.  Capture the explicit calls instead.  They have no
+forward-mode derivatives, and refuse inputs with tangents.
 
 Every step runs in ``libprism.so`` (contracts in ``include/prism.h``), on the current stream of the
 tensors' device.  Checks of shapes, types and devices raise ``ValueError``; what the library refuses
@@ -25,6 +26,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _abi
@@ -182,6 +184,11 @@ def _refuse_capture(name, instead):
 
 
 def _wants_graph(*tensors):
+    """Whether a gradient may be asked for.  Tangents of forward mode are refused: a result without them would be taken
+    for a constant."""
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None
+                                              for t in tensors):
+        raise NotImplementedError("no forward-mode derivatives")
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 

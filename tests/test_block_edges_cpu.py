@@ -4,6 +4,7 @@ import ctypes
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from dynamic_block_sparse_macro_b200 import _abi, block
 
@@ -32,6 +33,41 @@ def host(monkeypatch):
     monkeypatch.setattr(block, "_current", lambda index: True)
     monkeypatch.setattr(block, "_plans", {})
     return Through
+
+
+@pytest.fixture
+def unlaunched(L, host, monkeypatch):
+    """As ``host``, and every call of the library that would launch answers that it has."""
+    class Library:
+        def __getattr__(self, name):
+            return getattr(L, name) if name.endswith(("_bytes", "_sizes")) else lambda *a: OK
+    library = Library()
+    monkeypatch.setattr(_abi, "lib", lambda: library)
+    monkeypatch.setattr(block, "_stream", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+
+def test_tangents_of_forward_mode_are_refused(unlaunched):
+    """No result without its tangent, whichever input carries one, with or without gradients beside it."""
+    x, h, v, q, t = torch.zeros(6, 8), torch.zeros(6, 8), torch.zeros(1, 8), torch.zeros(6, 2, 64), torch.zeros(62, 2)
+    p = block.ExpertPlan(6, 2, 3, 1, 8, torch.device("cpu"))
+    ys, w, qw = torch.zeros(p.rows_sorted, 8), torch.zeros(6, 2), torch.ones(64)
+    kw = dict(grid=(1, 2, 3), axes=(12, 10, 10))
+    with forward_ad.dual_level():
+        dual = lambda a: forward_ad.make_dual(a, torch.ones_like(a))
+        for f in (lambda: block.norm(dual(x)), lambda: block.norm(x, dual(h)), lambda: block.norm(x, gate=None, scale=dual(v)),
+                  lambda: block.norm(x.clone().requires_grad_(), dual(h)),
+                  lambda: block.rotate(dual(q), None, t, **kw), lambda: block.rotate(q, dual(q), t, **kw),
+                  lambda: block.rotate(q, None, t, q_weight=dual(qw), **kw), lambda: block.dispatch(dual(x), p),
+                  lambda: block.combine(dual(ys), p), lambda: block.combine(ys, p, dual(w)),
+                  lambda: block.combine(ys, p, add=dual(x))):
+            with pytest.raises(NotImplementedError):
+                f()
+            with pytest.raises(NotImplementedError), torch.no_grad():
+                f()
+        # none of the inputs carries one
+        assert block.norm(x, h)[0].shape == x.shape and block.combine(ys, p, w).shape == x.shape
+    assert block.norm(x.clone().requires_grad_(), h)[0].requires_grad
 
 
 def test_an_output_that_is_also_a_second_input_is_refused(L, host):
