@@ -14,6 +14,9 @@ differentiable forms refuse to run under capture: autograd would tie the capture
 gradient accumulators that may belong to another stream.  Capture the explicit calls instead.  They have no
 forward-mode derivatives, and refuse inputs with tangents.
 
+Outputs given to the explicit calls are written in place: tensors that autograd has saved for a backward are known to
+have changed, and one that requires grad is refused outside of ``torch.no_grad()``.
+
 Every step runs in ``libprism.so`` (contracts in ``include/prism.h``), on the current stream of the
 tensors' device.  Checks of shapes, types and devices raise ``ValueError``; what the library refuses
 raises ``PrismError``.
@@ -27,6 +30,7 @@ import ctypes
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 from torch.autograd.function import once_differentiable
 
 from . import _abi
@@ -162,8 +166,21 @@ def _itself(a, b):
     return a.data_ptr() == b.data_ptr() and a.shape == b.shape and a.stride() == b.stride() and a.dtype == b.dtype
 
 
+def _writable(out, what):
+    _need(not (out.requires_grad and torch.is_grad_enabled()),
+          f"{what} requires grad and is written without autograd's knowledge: use torch.no_grad()")
+
+
+def _written(*outs):
+    """Tells autograd that given outputs have new values: a backward that needs the old ones then raises."""
+    for t in outs:
+        if t is not None and not t.is_inference():           # inference tensors have no version
+            increment_version(t)
+
+
 def _check_out(out, what, allowed, *others):
     """An output may be the tensor ``allowed`` itself, and has to be apart from all others."""
+    _writable(out, what)
     o0, o1 = _bytes(out)
     near = False
     for t in (allowed, *others):
@@ -279,6 +296,7 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
             return norm_forward(x, h, gate=gate, post_weight=post_weight, weight=weight, bias=bias, scale=scale,
                                 shift=shift, norm=norm, post_norm=post_norm, eps=eps, res_scale=res_scale,
                                 rows_per_group=rows_per_group, out_dtype=out_dtype, z=z, y=y)
+    given = (z, y)
     if z is not None:
         # h may be x, in place too: a row's h is read before its z is written
         _check_out(z, "z", x, None if _itself(h, x) else h, gate, post_weight, weight, bias, scale, shift)
@@ -291,6 +309,7 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
     _check("prism_block_norm_fwd", _abi.lib().prism_block_norm_fwd(
         p.addr, x.data_ptr(), _ptr(h), _ptr(gate), _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(scale),
         _ptr(shift), _ptr(z), _ptr(y), _stream(p.index)))
+    _written(*given)
     return (x if h is None else z), y
 
 
@@ -523,6 +542,8 @@ def rotate_forward(Q, K, table, *, grid, axes, q_weight=None, k_weight=None, nor
     _check("prism_head_rotate_fwd", _abi.lib().prism_head_rotate_fwd(
         p.addr, _ptr(Q), _ptr(K), _ptr(q_weight), _ptr(k_weight), table.data_ptr(), _ptr(oq), _ptr(ok),
         _stream(p.index)))
+    if out is not None:
+        _written(oq, ok)
     return oq, ok
 
 
@@ -720,6 +741,8 @@ def expert_dispatch(x, plan, *, out=None):
     clear = out is None
     if clear:
         out = torch.empty(plan.rows_sorted, C, dtype=x.dtype, device=x.device)
+    else:
+        _writable(out, "out")
     p_x, p_out = x.data_ptr(), out.data_ptr()
     if p_x < p_out + n_out and p_out < p_x + n_x:
         _check_out(out, "out", None, x)
@@ -727,6 +750,8 @@ def expert_dispatch(x, plan, *, out=None):
                                             plan.offsets.data_ptr(), clear, p_out, _stream(p.index))
     if code:
         raise _abi.PrismError("prism_expert_dispatch", code)
+    if not clear:
+        _written(out)
     return out
 
 
@@ -754,6 +779,7 @@ def expert_combine(ys, plan, weights=None, *, add=None, out=None):
         with torch.cuda.device(p.index):
             return expert_combine(ys, plan, weights, add=add, out=out)
     dt, C, ld_add, ld_out = p.a
+    given = out
     if out is None:
         out = torch.empty(plan.rows, C, dtype=ys.dtype, device=ys.device)
     else:
@@ -764,6 +790,7 @@ def expert_combine(ys, plan, weights=None, *, add=None, out=None):
                                            _stream(p.index))
     if code:
         raise _abi.PrismError("prism_expert_combine", code)
+    _written(given)
     return out
 
 
@@ -804,6 +831,7 @@ def expert_combine_backward(dout, ys, plan, weights=None, *, out=None, want_weig
         out = torch.empty(plan.rows_sorted, C, dtype=dout.dtype, device=dout.device)
         p_out = out.data_ptr()
     else:
+        _writable(out, "out")
         p_out = out.data_ptr()
         end = p_out + n_out
         if (p_d < end and p_out < p_d + n_d or p_y is not None and p_y < end and p_out < p_y + n_y
@@ -818,6 +846,8 @@ def expert_combine_backward(dout, ys, plan, weights=None, *, out=None, want_weig
                                                _stream(p.index))
     if code:
         raise _abi.PrismError("prism_expert_combine_bwd", code)
+    if not clear:
+        _written(out)
     return out, dw
 
 

@@ -70,6 +70,62 @@ def test_tangents_of_forward_mode_are_refused(unlaunched):
     assert block.norm(x.clone().requires_grad_(), h)[0].requires_grad
 
 
+def given_outputs():
+    """(name, output, call that writes it) of every output that a caller may give, in place or apart."""
+    z = lambda *s: torch.zeros(*s)
+    t = torch.zeros(62, 2)
+    p, kw = block.ExpertPlan(6, 2, 3, 1, 8, torch.device("cpu")), dict(grid=(1, 2, 3), axes=(12, 10, 10))
+    n = p.rows_sorted
+    return [
+        ("z", z(6, 8), lambda o: block.norm_forward(z(6, 8), z(6, 8), z=o)),
+        ("z is x", z(6, 8), lambda o: block.norm_forward(o, z(6, 8), z=o)),
+        ("y", z(6, 8), lambda o: block.norm_forward(z(6, 8), y=o)),
+        ("a part of y's buffer", z(6, 24)[:, 8:16], lambda o: block.norm_forward(z(6, 8), y=o)),
+        ("y, of a copied input", z(6, 8), lambda o: block.norm_forward(z(8, 6).t(), y=o)),
+        ("Qr", z(6, 2, 64), lambda o: block.rotate_forward(z(6, 2, 64), None, t, out=(o, None), **kw)),
+        ("Kr is K", z(6, 2, 64), lambda o: block.rotate_forward(z(6, 2, 64), o, t, out=(z(6, 2, 64), o), **kw)),
+        ("xs", z(n, 8), lambda o: block.expert_dispatch(z(6, 8), p, out=o)),
+        ("combined", z(6, 8), lambda o: block.expert_combine(z(n, 8), p, out=o)),
+        ("combined is add", z(6, 8), lambda o: block.expert_combine(z(n, 8), p, add=o, out=o)),
+        ("dys", z(n, 8), lambda o: block.expert_combine_backward(z(6, 8), z(n, 8), p, out=o)),
+        ("dys is ys", z(n, 8), lambda o: block.expert_combine_backward(z(6, 8), o, p, out=o)),
+    ]
+
+
+@pytest.mark.parametrize("i", range(12))
+def test_autograd_knows_of_given_outputs(unlaunched, i):
+    name, o, call = given_outputs()[i]
+    # a tensor that autograd has saved: the call goes through, the backward that needs its old values does not
+    a = torch.ones_like(o).requires_grad_()
+    prod = (a * o).sum()
+    before = o._version
+    call(o)
+    assert o._version > before, name
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        prod.backward()
+    call(o)                                                # kept signatures behave alike
+    assert o._version > before + 1, name
+    # a leaf, and a tensor with a history
+    for g in (given_outputs()[i][1].requires_grad_(), given_outputs()[i][1].requires_grad_() * 1):
+        with pytest.raises(ValueError, match="requires grad"):
+            call(g)
+        with torch.no_grad():
+            call(g)
+    with torch.inference_mode():
+        call(given_outputs()[i][1])
+
+
+def test_results_that_are_not_given_keep_their_version(unlaunched):
+    x, h = torch.zeros(6, 8), torch.zeros(6, 8)
+    z, y = block.norm_forward(x, h)
+    assert x._version == h._version == 0
+    x = x.clone().requires_grad_()
+    z, y = block.norm(x, h)
+    block.norm_forward(x, h)
+    (z.sum() + y.sum()).backward()
+    assert x.grad is not None
+
+
 def test_an_output_that_is_also_a_second_input_is_refused(L, host):
     """With one choice a token and no padding, sorted and token buffers have one shape, and the tensor that an output
     may take the place of can be another argument too, which other tokens still read."""
