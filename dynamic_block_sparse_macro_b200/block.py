@@ -27,6 +27,7 @@ made once a signature and kept (``_plans``), so that a repeated call costs littl
 from __future__ import annotations
 
 import ctypes
+from operator import index
 
 import torch
 from torch.autograd import forward_ad
@@ -48,6 +49,24 @@ _MAX_PLANS = 2048
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
+
+
+def _real(v, what):
+    """A number that a kept call holds: its value now, where it is a tensor of one element."""
+    if type(v) is float:
+        return v
+    _need(not (isinstance(v, torch.Tensor) and v.requires_grad), f"{what} is a number and gets no gradient")
+    return float(v)
+
+
+def _group_rows(v):
+    return None if v is None else int(v)
+
+
+def _whole(values):
+    _need(len(values) == 3, "grid and axes have three entries: (T, H, W)")
+    a, b, c = values
+    return (a, b, c) if type(a) is type(b) is type(c) is int else (index(a), index(b), index(c))
 
 
 def _sig(t):
@@ -236,7 +255,7 @@ def _norm_plan(x, h, gate, post_weight, weight, bias, scale, shift, norm, post_n
     if rpg is None:
         rpg = x.shape[-2] if x.dim() > 2 else R
     _need(rpg >= 1 or R == 0, "rows_per_group must be at least 1")
-    rpg = max(1, int(rpg))
+    rpg = max(1, rpg)
     G = -(-R // rpg)
     for v, shape, what in ((gate, (G, C), "gate"), (scale, (G, C), "scale"), (shift, (G, C), "shift"),
                            (post_weight, (C,), "post_weight"), (weight, (C,), "weight"), (bias, (C,), "bias")):
@@ -270,6 +289,7 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
     three or more, else all rows); weight, bias and post_weight float32 [C].  ``norm=None`` gives no y.  y has
     ``out_dtype`` (default: h's type, else x's).  ``z`` and ``y`` may be given as outputs; z may be x itself.
     """
+    eps, res_scale, rows_per_group = _real(eps, "eps"), _real(res_scale, "res_scale"), _group_rows(rows_per_group)
     key = ("norm", x.shape, x.stride(), x.dtype, x.device, _sig(h), _sig(gate), _sig(post_weight), _sig(weight), _sig(bias),
            _sig(scale), _sig(shift), norm, post_norm, eps, res_scale, rows_per_group, out_dtype, _sig(z), _sig(y))
     p = _plans.get(key)
@@ -327,6 +347,7 @@ def norm_backward(z, h, dz, dy, *, gate=None, post_weight=None, weight=None, bia
     """
     if wants is not None:
         wants = tuple(wants)
+    eps, res_scale, rows_per_group = _real(eps, "eps"), _real(res_scale, "res_scale"), _group_rows(rows_per_group)
     key = ("dnorm", z.shape, z.stride(), z.dtype, z.device, _sig(h), _sig(dz), _sig(dy), _sig(gate), _sig(post_weight),
            _sig(weight), _sig(bias), _sig(scale), norm, post_norm, eps, res_scale, rows_per_group, wants)
     p = _plans.get(key)
@@ -408,7 +429,8 @@ def norm(x, h=None, *, gate=None, post_weight=None, weight=None, bias=None, scal
          post_norm=None, eps=1e-6, res_scale=1.0, rows_per_group=None, out_dtype=None):
     """Differentiable ``norm_forward``: returns (z, y); z is x itself where there is no h."""
     tensors = (x, h, gate, post_weight, weight, bias, scale, shift)
-    kw = dict(norm=norm, post_norm=post_norm, eps=eps, res_scale=res_scale, rows_per_group=rows_per_group)
+    kw = dict(norm=norm, post_norm=post_norm, eps=_real(eps, "eps"), res_scale=_real(res_scale, "res_scale"),
+              rows_per_group=_group_rows(rows_per_group))
     if not _wants_graph(*tensors):
         return norm_forward(x, h, gate=gate, post_weight=post_weight, weight=weight, bias=bias, scale=scale,
                             shift=shift, out_dtype=out_dtype, **kw)
@@ -464,7 +486,6 @@ def _on16(*tensors):
 def _rotate_plan(ins, outs, table, grid, axes, weights, norm, eps, pairs):
     """ins, outs: pairs of tensors (Q's, K's) by descriptor fields, the first of ins deciding the shapes."""
     _need(pairs in _PAIRS, f"pairs is 'interleaved' or 'half', not {pairs!r}")
-    _need(len(grid) == 3 and len(axes) == 3, "grid and axes have three entries: (T, H, W)")
     tensors = [t for f, pair in (*ins, *outs) for t in pair if t is not None]
     _need(tensors, "neither Q nor K")
     first = tensors[0]
@@ -492,7 +513,7 @@ def _rotate_plan(ins, outs, table, grid, axes, weights, norm, eps, pairs):
         for t, n in zip(pair, heads):
             _need(t is None or t.shape[1] == n, "Q and K must be like their gradients and results")
     desc = _abi.RotateT(first.shape[0], *grid, *heads, first.shape[2], *axes, _PAIRS[pairs], _DT[first.dtype],
-                        int(bool(norm)), eps, *(lds.get(f, 0) for f in ("q", "k", "qo", "ko", "dq", "dk")))
+                        int(norm), eps, *(lds.get(f, 0) for f in ("q", "k", "qo", "ko", "dq", "dk")))
     p = _Plan(desc, first.device, copy)
     p.ws_bytes = _abi.head_rotate_ws_bytes(desc)
     return p
@@ -508,7 +529,8 @@ def rotate_forward(Q, K, table, *, grid, axes, q_weight=None, k_weight=None, nor
     heads.  ``out`` = (Qr, Kr) takes the results, and may be (Q, K) themselves.
     """
     oq, ok = (None, None) if out is None else out
-    key = ("rotate", _sig(Q), _sig(K), _sig(table), tuple(grid), tuple(axes), _sig(q_weight), _sig(k_weight), norm, eps,
+    grid, axes, norm, eps = _whole(grid), _whole(axes), bool(norm), _real(eps, "eps")
+    key = ("rotate", _sig(Q), _sig(K), _sig(table), grid, axes, _sig(q_weight), _sig(k_weight), norm, eps,
            pairs, _sig(oq), _sig(ok))
     p = _plans.get(key)
     if p is None:
@@ -554,10 +576,11 @@ def rotate_backward(Q, K, dQr, dKr, table, *, grid, axes, q_weight=None, k_weigh
     others are None.  Without a norm Q and K are not read and may be None."""
     if wants is not None:
         wants = tuple(wants)
+    grid, axes, norm, eps = _whole(grid), _whole(axes), bool(norm), _real(eps, "eps")
     if not norm:
         Q = K = None
-    key = ("drotate", _sig(Q), _sig(K), _sig(dQr), _sig(dKr), _sig(table), tuple(grid), tuple(axes), _sig(q_weight),
-           _sig(k_weight), norm, eps, pairs, wants)
+    key = ("drotate", _sig(Q), _sig(K), _sig(dQr), _sig(dKr), _sig(table), grid, axes, _sig(q_weight), _sig(k_weight),
+           norm, eps, pairs, wants)
     p = _plans.get(key)
     if p is None:
         for x, dr in ((Q, dQr), (K, dKr)):
@@ -625,7 +648,7 @@ class _RotateFn(torch.autograd.Function):
 
 def rotate(Q, K, table, *, grid, axes, q_weight=None, k_weight=None, norm=True, eps=1e-6, pairs="interleaved"):
     """Differentiable ``rotate_forward`` (the table gets no gradient)."""
-    kw = dict(grid=tuple(grid), axes=tuple(axes), norm=norm, eps=eps, pairs=pairs)
+    kw = dict(grid=_whole(grid), axes=_whole(axes), norm=bool(norm), eps=_real(eps, "eps"), pairs=pairs)
     if not _wants_graph(Q, K, q_weight, k_weight):
         return rotate_forward(Q, K, table, q_weight=q_weight, k_weight=k_weight, **kw)
     _refuse_capture("block.rotate", "rotate_forward and rotate_backward")

@@ -70,6 +70,62 @@ def test_tangents_of_forward_mode_are_refused(unlaunched):
     assert block.norm(x.clone().requires_grad_(), h)[0].requires_grad
 
 
+def test_numbers_held_in_tensors_are_read_at_each_call(unlaunched, monkeypatch):
+    """A number may come in a tensor of one element, whose value may change between two calls of one signature."""
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            of = {"prism_block_norm_fwd": _abi.BlockNormT, "prism_block_norm_bwd": _abi.BlockNormT,
+                  "prism_head_rotate_fwd": _abi.RotateT, "prism_head_rotate_bwd": _abi.RotateT}.get(name)
+            if of is None:
+                return getattr(answering, name)
+            return lambda addr, *a: seen.append(of.from_buffer_copy(ctypes.string_at(addr, ctypes.sizeof(of)))) or OK
+    answering, library = _abi.lib(), Library()
+    monkeypatch.setattr(_abi, "lib", lambda: library)
+    x, h, q, t = torch.zeros(6, 8), torch.zeros(6, 8), torch.zeros(6, 2, 64), torch.zeros(62, 2)
+    n = {k: torch.tensor(v) for k, v in dict(eps=0.25, res_scale=0.5, rows_per_group=2).items()}
+    grid, norm = [torch.tensor(v) for v in (1, 2, 3)], torch.tensor(True)
+    for f in (lambda: block.norm_forward(x, h, **n), lambda: block.norm_backward(x, h, x, x, **n),
+              lambda: block.norm(x, h, **n)):
+        for scale in (0.5, 2.0):
+            n["res_scale"].fill_(scale)
+            n["eps"].fill_(scale / 8)
+            n["rows_per_group"].fill_(int(2 * scale))
+            f()
+            assert (seen[-1].res_scale, seen[-1].eps, seen[-1].rows_per_group) == (scale, scale / 8, int(2 * scale))
+    for f in (lambda: block.rotate_forward(q, None, t, grid=grid, axes=(12, 10, 10), norm=norm),
+              lambda: block.rotate_backward(q, None, q, None, t, grid=grid, axes=(12, 10, 10), norm=norm)):
+        for T, H, flag in ((1, 2, True), (1, 2, False), (1, 2, True)):
+            norm.fill_(flag)
+            f()
+            assert (seen[-1].T, seen[-1].H, seen[-1].norm) == (T, H, flag)
+    t2 = torch.zeros(6, 2)
+    for T, H in ((2, 3), (6, 1)):
+        grid[0].fill_(T), grid[1].fill_(H)
+        block.rotate_forward(q, None, t2[:T], grid=grid, axes=(1, 0, 0))
+        assert (seen[-1].T, seen[-1].H) == (T, H)
+        block.rotate_forward(q, None, t2, grid=[T, 6, 1], axes=(0, 1, 0))
+        assert seen[-1].T == T
+    grid = [torch.tensor(v) for v in (2, 1, 1)]
+    for T in (2, 5):
+        grid[0].fill_(T)
+        block.rotate_forward(q, None, t2[:1], grid=grid, axes=(0, 0, 1))
+        assert seen[-1].T == T
+    # the differentiable form's backward has the forward's numbers
+    n = {k: torch.tensor(v) for k, v in dict(eps=0.25, res_scale=0.5, rows_per_group=6).items()}
+    z, _ = block.norm(x.clone().requires_grad_(), h, **n)
+    n["res_scale"].fill_(3.0)
+    z.sum().backward()
+    assert seen[-1].res_scale == 0.5
+    with pytest.raises(ValueError, match="three"):
+        block.rotate(q, None, t, grid=(1, 2, 3, 1), axes=(12, 10, 10))
+    # a number that is to be learned would get no gradient
+    for k in ("eps", "res_scale"):
+        with pytest.raises(ValueError, match="gradient"):
+            block.norm(x, h, **{k: torch.tensor(0.5, requires_grad=True)})
+
+
 def given_outputs():
     """(name, output, call that writes it) of every output that a caller may give, in place or apart."""
     z = lambda *s: torch.zeros(*s)
