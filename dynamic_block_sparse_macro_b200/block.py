@@ -59,6 +59,12 @@ def _real(v, what):
     return float(v)
 
 
+def _fits(**fields):
+    """A descriptor's 32-bit fields, which would take the low half of a larger number."""
+    for name, v in fields.items():
+        _need(abs(v) < 1 << 31, f"{name} = {v} is out of range")
+
+
 def _group_rows(v):
     return None if v is None else int(v)
 
@@ -244,6 +250,7 @@ def _norm_plan(x, h, gate, post_weight, weight, bias, scale, shift, norm, post_n
     _need(x.dim() >= 1 and x.shape[-1] >= 1, f"x must be [..., C], not {tuple(x.shape)}")
     _need(x.dtype in _DT and branch in _DT, f"float32 or bfloat16, not {x.dtype} and {branch}")
     C, R, dev = x.shape[-1], _count(x.shape), x.device
+    _fits(channels=C)
     _same_device(dev, h, gate, post_weight, weight, bias, scale, shift, *(t for _, _, t, _ in rows))
     if h is not None:
         _need(h.shape == x.shape, f"h must have x's shape {tuple(x.shape)}, not {tuple(h.shape)}")
@@ -255,7 +262,7 @@ def _norm_plan(x, h, gate, post_weight, weight, bias, scale, shift, norm, post_n
     if rpg is None:
         rpg = x.shape[-2] if x.dim() > 2 else R
     _need(rpg >= 1 or R == 0, "rows_per_group must be at least 1")
-    rpg = max(1, rpg)
+    rpg = min(max(1, rpg), max(1, R))
     G = -(-R // rpg)
     for v, shape, what in ((gate, (G, C), "gate"), (scale, (G, C), "scale"), (shift, (G, C), "shift"),
                            (post_weight, (C,), "post_weight"), (weight, (C,), "weight"), (bias, (C,), "bias")):
@@ -512,6 +519,8 @@ def _rotate_plan(ins, outs, table, grid, axes, weights, norm, eps, pairs):
     for _, pair in (*ins[1:], *outs):
         for t, n in zip(pair, heads):
             _need(t is None or t.shape[1] == n, "Q and K must be like their gradients and results")
+    T, H, W = grid
+    _fits(T=T, H=H, W=W, pairs_t=axes[0], pairs_h=axes[1], pairs_w=axes[2], head_dim=first.shape[2], heads=max(heads))
     desc = _abi.RotateT(first.shape[0], *grid, *heads, first.shape[2], *axes, _PAIRS[pairs], _DT[first.dtype],
                         int(norm), eps, *(lds.get(f, 0) for f in ("q", "k", "qo", "ko", "dq", "dk")))
     p = _Plan(desc, first.device, copy)
@@ -671,6 +680,7 @@ class ExpertPlan:
         key = ("experts", rows, top_k, experts, align, id_bytes, device)
         p = _plans.get(key)
         if p is None:
+            _fits(top_k=top_k, experts=experts, align=align)
             p = _Plan(_abi.ExpertsT(rows, top_k, experts, align, id_bytes), device)
             p.a, p.ws_bytes = _abi.expert_sizes(p.desc)
             _keep(key, p)

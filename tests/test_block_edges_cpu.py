@@ -126,6 +126,29 @@ def test_numbers_held_in_tensors_are_read_at_each_call(unlaunched, monkeypatch):
             block.norm(x, h, **{k: torch.tensor(0.5, requires_grad=True)})
 
 
+def test_numbers_past_the_descriptors_32_bits_are_refused(unlaunched):
+    """2^32 and a small number, which would be taken for the small one: sizes of expanded tensors, of which nothing but
+    the shape is looked at."""
+    big = (1 << 32) + 8
+    x, h = torch.zeros(6, 8), torch.zeros(6, 8)
+    q, t = torch.zeros(6, 2, 64), torch.zeros(62, 2)
+    wide = torch.zeros(1, 1).expand(1, big)
+    for f in (lambda: block.norm_forward(wide), lambda: block.norm_backward(wide, None, None, wide),
+              lambda: block.rotate_forward(torch.zeros(1, 1, 1).expand(1, 1, (1 << 32) + 64), None, t[:0],
+                                           grid=(1, 1, 1), axes=(0, 0, 0)),
+              lambda: block.rotate_forward(torch.zeros(1, 1, 1).expand(1, (1 << 32) + 1, 64), None, t[:0],
+                                           grid=(1, 1, 1), axes=(0, 0, 0)),
+              lambda: block.rotate_forward(q, None, t[:12], grid=(1, (1 << 32) + 2, 3), axes=(12, 0, 0)),
+              lambda: block.expert_plan(torch.zeros(6, 2, dtype=torch.int64), big),
+              lambda: block.expert_plan(torch.zeros(6, 2, dtype=torch.int64), 8, align=(1 << 32) + 1),
+              lambda: block.ExpertPlan(6, (1 << 32) + 2, 8, 1, 8, torch.device("cpu"))):
+        with pytest.raises(ValueError, match="out of range"):
+            f()
+    # more rows a group than there are rows, however many, are all of them
+    z, y = block.norm_forward(x, h, gate=torch.zeros(1, 8), rows_per_group=(1 << 64) + 2)
+    assert z.shape == x.shape
+
+
 def given_outputs():
     """(name, output, call that writes it) of every output that a caller may give, in place or apart."""
     z = lambda *s: torch.zeros(*s)
