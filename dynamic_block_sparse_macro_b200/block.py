@@ -264,6 +264,10 @@ def _norm_plan(x, h, gate, post_weight, weight, bias, scale, shift, norm, post_n
     _need(rpg >= 1 or R == 0, "rows_per_group must be at least 1")
     rpg = min(max(1, rpg), max(1, R))
     G = -(-R // rpg)
+    if R == 0:
+        # groups without rows: as many as the vectors have, or as x's leading dimensions make
+        G = next((v.shape[0] for v in (gate, scale, shift) if v is not None and v.dim() == 2),
+                 _count(x.shape[:-1]) if x.dim() > 2 and rows_per_group is None else 0)
     for v, shape, what in ((gate, (G, C), "gate"), (scale, (G, C), "scale"), (shift, (G, C), "shift"),
                            (post_weight, (C,), "post_weight"), (weight, (C,), "weight"), (bias, (C,), "bias")):
         _vector(v, shape, what)
@@ -293,7 +297,7 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
 
     x [..., C] is the residual stream, h [..., C] the block's output (None: z is x); gate, scale and shift are
     float32 [groups, C], one row for each ``rows_per_group`` rows (default: x's last-but-one dimension where it has
-    three or more, else all rows); weight, bias and post_weight float32 [C].  ``norm=None`` gives no y.  y has
+    three or more, else all rows; without rows any number of groups); weight, bias and post_weight float32 [C].  ``norm=None`` gives no y.  y has
     ``out_dtype`` (default: h's type, else x's).  ``z`` and ``y`` may be given as outputs; z may be x itself.
     """
     eps, res_scale, rows_per_group = _real(eps, "eps"), _real(res_scale, "res_scale"), _group_rows(rows_per_group)
@@ -389,8 +393,9 @@ def norm_backward(z, h, dz, dy, *, gate=None, post_weight=None, weight=None, bia
         g["dh"] = _like(z, p.a)
     groups, vectors = p.c
     G, C = p.b
+    make = torch.empty if p.desc.rows else torch.zeros           # the library has no groups where it has no rows
     for n in groups:
-        g[n] = torch.empty(G, C, dtype=torch.float32, device=dev)
+        g[n] = make(G, C, dtype=torch.float32, device=dev)
     for n in vectors:
         g[n] = torch.empty(C, dtype=torch.float32, device=dev)
     ws = torch.empty(p.ws_bytes, dtype=torch.uint8, device=dev) if groups or vectors else None
@@ -408,7 +413,7 @@ class _NormFn(torch.autograd.Function):
         z, y = norm_forward(x, h, gate=gate, post_weight=post_weight, weight=weight, bias=bias, scale=scale,
                             shift=shift, out_dtype=out_dtype, **kw)
         ctx.save_for_backward(z, h, gate, post_weight, weight, bias, scale)
-        ctx.kw, ctx.y_dtype = kw, None if y is None else y.dtype
+        ctx.kw, ctx.y_dtype, ctx.shift = kw, None if y is None else y.dtype, None if shift is None else shift.shape
         return (z, y) if h is not None else y
 
     @staticmethod
@@ -428,6 +433,8 @@ class _NormFn(torch.autograd.Function):
                                 ("dshift", 7)) if need[k]]
         g = norm_backward(z, h, dz, dy, gate=gate, post_weight=post_weight, weight=weight, bias=bias, scale=scale,
                           wants=wants, **ctx.kw)
+        if g["dshift"] is not None and g["dshift"].shape != ctx.shift:       # without rows its groups are not known
+            g["dshift"] = g["dshift"].new_zeros(ctx.shift)
         return (g["dx"] if need[0] else None, g["dh"] if need[1] else None, g["dgate"], g["dpost_weight"], g["dweight"],
                 g["dbias"], g["dscale"], g["dshift"], None, None)
 

@@ -149,6 +149,26 @@ def test_numbers_past_the_descriptors_32_bits_are_refused(unlaunched):
     assert z.shape == x.shape
 
 
+@pytest.mark.parametrize("shape,rpg,G", [((2, 0, 8), None, 2), ((2, 0, 8), 5, 3), ((0, 4, 8), None, 0), ((0, 8), None, 1),
+                                         ((0, 8), 7, 2), ((0, 8), None, 0), ((3, 2, 0, 8), None, 6)])
+def test_groups_without_rows_have_their_vectors_and_gradients(unlaunched, shape, rpg, G):
+    """Samples of no tokens: a row of gate, scale and shift each, whose gradients are 0."""
+    x, h = torch.zeros(shape, requires_grad=True), torch.zeros(shape)
+    for names in (("gate", "scale", "shift"), ("shift",), ("scale",)):
+        v = {k: torch.ones(G, 8, requires_grad=True) for k in names}
+        z, y = block.norm(x, h, rows_per_group=rpg, **v)
+        assert z.shape == y.shape == shape
+        (z.sum() + y.sum()).backward()
+        for k in names:
+            assert torch.equal(v[k].grad, torch.zeros(G, 8)), k
+    g = block.norm_backward(x.detach(), h, h, h, gate=torch.ones(G, 8), scale=torch.ones(G, 8), rows_per_group=rpg)
+    assert all(torch.equal(g[k], torch.zeros(G, 8)) for k in ("dgate", "dscale", "dshift"))
+    if shape == (3, 2, 0, 8):
+        assert block.norm_backward(x.detach(), None, None, h, wants=("dshift",))["dshift"].shape == (6, 8)
+    with pytest.raises(ValueError):
+        block.norm_forward(x.detach(), h, gate=torch.ones(G, 8), scale=torch.ones(G + 1, 8), rows_per_group=rpg)
+
+
 def given_outputs():
     """(name, output, call that writes it) of every output that a caller may give, in place or apart."""
     z = lambda *s: torch.zeros(*s)
