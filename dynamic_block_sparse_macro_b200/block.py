@@ -221,7 +221,7 @@ def _check_out(out, what, allowed, *others):
 
 
 def _refuse_capture(name, instead):
-    if torch.cuda.is_current_stream_capturing():
+    if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
         raise RuntimeError(f"{name} works on an autograd graph and cannot be captured; capture {instead}")
 
 

@@ -19,6 +19,14 @@ def L():
     return _abi.lib()
 
 
+def test_leaves_off_the_gpu_are_refused_as_other_tensors_are():
+    x, q = torch.zeros(4, 8, requires_grad=True), torch.zeros(4, 2, 64, requires_grad=True)
+    for f in (lambda: block.norm(x), lambda: block.norm(x.detach(), x),
+              lambda: block.rotate(q, None, torch.zeros(1, 2), grid=(1, 1, 1), axes=(1, 0, 0))):
+        with pytest.raises(ValueError, match="CUDA"):
+            f()
+
+
 @pytest.fixture
 def host(monkeypatch):
     """The tensor calls on CPU tensors, up to the library: the device check is passed over, and a call that gets
@@ -44,7 +52,6 @@ def unlaunched(L, host, monkeypatch):
     library = Library()
     monkeypatch.setattr(_abi, "lib", lambda: library)
     monkeypatch.setattr(block, "_stream", lambda index: 0)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
 
 
 def test_tangents_of_forward_mode_are_refused(unlaunched):
