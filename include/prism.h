@@ -569,7 +569,8 @@ prism_status_t prism_block_norm_bwd(const prism_block_norm_t* n, const void* z, 
  * rotation of the head's d/2 channel pairs by angles that depend on the
  * token's place (t, h, w) in the T x H x W grid.  Token i has place i mod
  * (T H W), in raster order.  The first pairs_t pairs turn with t, the next
- * pairs_h with h, the next pairs_w with w; the rest do not turn.
+ * pairs_h with h, the next pairs_w with w; the rest do not turn: their channels
+ * go through by themselves, infinities and NaN included.
  *    table: float32 (cos, sin) pairs, [T][pairs_t], then [H][pairs_h], then
  *           [W][pairs_w] (positions and frequencies are the caller's)
  *    pairs: INTERLEAVED channels (2i, 2i+1), HALF channels (i, i + d/2)

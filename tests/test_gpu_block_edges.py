@@ -9,6 +9,8 @@ from dynamic_block_sparse_macro_b200 import _abi, block
 
 pytestmark = pytest.mark.gpu
 
+F32, BF16 = torch.float32, torch.bfloat16
+
 
 def gen(seed):
     g = torch.Generator(device="cuda")
@@ -53,3 +55,43 @@ def test_threads_in_one_kernel_with_rows_of_other_widths(widths):
     assert codes == [{0}] * len(widths)
     for _, _, _, _, _, outs, want in calls:
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+# ------------------------------------------------------------------ rotation
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("pairs", ["interleaved", "half"])
+@pytest.mark.parametrize("d,axes", [(64, (8, 8, 7)), (64, (0, 0, 0)), (128, (20, 20, 20)), (128, (0, 5, 0))])
+def test_a_pair_that_does_not_turn_is_left_alone(d, axes, pairs, dt):
+    """An infinity or NaN in one member of such a pair does not reach the other: without a norm the channels of these
+    pairs are copied, forwards and backwards."""
+    g = gen(d)
+    N, grid, n = 24, (2, 3, 4), sum(axes)
+    table = block.rotation_table(grid, axes)
+    x = torch.randn(N, 5, d, generator=g, device="cuda").to(dt)
+    ch = torch.arange(d, device="cuda")
+    pair = ch // 2 if pairs == "interleaved" else ch % (d // 2)
+    second = ch % 2 == 1 if pairs == "interleaved" else ch >= d // 2
+    still = pair >= n
+    y = x.clone()
+    y[0:8, :, still & second] = float("inf")
+    y[8:16, :, still & ~second] = float("-inf")
+    y[16:24, :, still & second] = float("nan")
+    kw = dict(grid=grid, axes=axes, norm=False, pairs=pairs)
+    same = lambda a, b: torch.equal(a.nan_to_num(7.0, 8.0, 9.0), b.nan_to_num(7.0, 8.0, 9.0))
+    for call in (lambda t: block.rotate_forward(t, None, table, **kw)[0],
+                 lambda t: block.rotate_backward(None, None, t, None, table, **kw)["dQ"]):
+        a, b = call(x), call(y)
+        assert torch.equal(a[..., still], x[..., still])
+        assert same(b[..., still], y[..., still]) and torch.equal(b[..., ~still], a[..., ~still])
+    # with the norm an infinity makes the row's root mean square infinite: it becomes NaN and all else 0
+    y = x.clone()
+    y[:, :, still & second] = float("inf")
+    out = block.rotate_forward(y, None, table, grid=grid, axes=axes, pairs=pairs)[0]
+    assert bool((out[..., still & ~second] == 0).all()) and bool(out[..., still & second].isnan().all())
+    assert bool((out[..., ~still] == 0).all())
+    # nor does an infinite weight
+    w = torch.ones(d, device="cuda")
+    w[still & second] = float("inf")
+    out = block.rotate_forward(x, None, table, grid=grid, axes=axes, pairs=pairs, q_weight=w)[0]
+    assert torch.equal(out[..., still & ~second], block.rotate_forward(x, None, table, grid=grid, axes=axes,
+                                                                       pairs=pairs)[0][..., still & ~second])
