@@ -141,8 +141,7 @@ __device__ __forceinline__ void angles(const Args& a, uint32_t token, int l, F2 
 // Pairs from `turn` on do not turn (STILL: there are some).  A sine of 0 does for finite values, but an infinity or NaN
 // times it is NaN, so what is to be multiplied by it is taken as 0 there, of the lane's pairs 2i and 2i + 1.  Forwards
 // at every head; backwards only where a head's sum shows a value that is not finite.  61440 x 24 x 128 bf16 interleaved,
-// 53 of 64 pairs turning: 266 us forwards (with the sine alone 252), backwards 431 (402) and by selection 436; with all
-// 64 turning 248 and 391.
+// 53 of 64 pairs turning: 261 us forwards (with the sine alone 249), 418 backwards (394; by selection 436).
 template <bool STILL> __device__ __forceinline__ F2 turning(int turn, int l, int i, F2 v) {
     if constexpr (!STILL) return v;
     const float2 f = both(v);
@@ -325,7 +324,8 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
                 if (a.norm) {
                     if constexpr (S > 0) CP::read(px[u], row);
                     v = pairs_of<T, HALF>(px[u]);
-                    // x once against itself, once against dn ∘ w; dx = r dn ∘ w - x r³ mean(dn ∘ w ∘ x)
+                    // x once against itself, once against dn ∘ w; dx = r (dn ∘ w - x r (r mean(dn ∘ w ∘ x))): r may be as
+                    // large as eps^-1/2, and meets what makes it small again before its next power
                     Pairs t;
                     F2 q2 = v.a[0] * v.a[0], m2;
 #pragma unroll
@@ -340,15 +340,15 @@ __global__ void __launch_bounds__(256, ctas_sm(sizeof(T), BWD)) k_head_rotate(co
                     float q = sum(q2), m = sum(m2);
                     lanes_sum<LPH>(q, m, l);
                     const float r = rsqrtf(q * (1.f / D) + a.eps);
-                    const F2 r2 = f2(r), k = f2(-(r * r) * (r * m) * (1.f / D));
+                    const F2 r2 = f2(r), k = f2(-(r * m * (1.f / D)) * r);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         if (in) {
                             dw.a[i] = fma(t.a[i], r2, dw.a[i]);
                             dw.b[i] = fma(t.b[i], r2, dw.b[i]);
                         }
-                        o.a[i] = fma(v.a[i], k, o.a[i] * w.a[i] * r2);
-                        o.b[i] = fma(v.b[i], k, o.b[i] * w.b[i] * r2);
+                        o.a[i] = fma(v.a[i], k, o.a[i] * w.a[i]) * r2;
+                        o.b[i] = fma(v.b[i], k, o.b[i] * w.b[i]) * r2;
                     }
                 }
             }

@@ -5,6 +5,7 @@ import threading
 import pytest
 import torch
 
+import block_forms as bf
 from dynamic_block_sparse_macro_b200 import _abi, block
 
 pytestmark = pytest.mark.gpu
@@ -95,3 +96,19 @@ def test_a_pair_that_does_not_turn_is_left_alone(d, axes, pairs, dt):
     out = block.rotate_forward(x, None, table, grid=grid, axes=axes, pairs=pairs, q_weight=w)[0]
     assert torch.equal(out[..., still & ~second], block.rotate_forward(x, None, table, grid=grid, axes=axes,
                                                                        pairs=pairs)[0][..., still & ~second])
+
+
+@pytest.mark.parametrize("pairs", ["interleaved", "half"])
+def test_rotation_backward_of_rows_of_zeros_with_the_smallest_eps(pairs):
+    """dx = r c for rows of zeros, r = eps^-1/2 up to 10^21: r is squared only with what makes it small again."""
+    g = gen(77)
+    grid, axes, eps = (1, 4, 4), (10, 11, 11), 1e-42
+    table = block.rotation_table(grid, axes)
+    x, dr = torch.zeros(16, 2, 64, device="cuda"), torch.randn(16, 2, 64, generator=g, device="cuda") * 1e-10
+    got = block.rotate_backward(x, None, dr, None, table, grid=grid, axes=axes, eps=eps, pairs=pairs)["dQ"]
+    cos, sin = bf.angles(table, grid, axes, 16, 64)
+    r = torch.tensor(eps, dtype=F32).double().item() ** -0.5
+    want = bf.rotate(dr.double(), None, cos, -sin, pairs, 0) * r
+    terms = dr.double().abs().amax() * 2 * r
+    # two products and a sum, the reciprocal root (four half steps), a product with it and one with the weight: 9
+    assert bool(((got.double() - want).abs() <= 9 * bf.U * terms).all())
