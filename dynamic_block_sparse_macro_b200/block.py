@@ -83,6 +83,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _there(t):
+    """As ``_ptr``, where the library is to see that a tensor is given: one without elements has no address of its own."""
+    return None if t is None else t.data_ptr() or 256
+
+
 def _keep(key, plan):
     """Keeps a finished plan: another thread may take it at once."""
     if len(_plans) >= _MAX_PLANS:
@@ -338,7 +343,7 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
     elif p.a:
         y = _like(x, p.c)
     _check("prism_block_norm_fwd", _abi.lib().prism_block_norm_fwd(
-        p.addr, x.data_ptr(), _ptr(h), _ptr(gate), _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(scale),
+        p.addr, x.data_ptr(), _there(h), _ptr(gate), _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(scale),
         _ptr(shift), _ptr(z), _ptr(y), _stream(p.index)))
     _written(*given)
     return (x if h is None else z), y
@@ -400,7 +405,7 @@ def norm_backward(z, h, dz, dy, *, gate=None, post_weight=None, weight=None, bia
         g[n] = torch.empty(C, dtype=torch.float32, device=dev)
     ws = torch.empty(p.ws_bytes, dtype=torch.uint8, device=dev) if groups or vectors else None
     _check("prism_block_norm_bwd", _abi.lib().prism_block_norm_bwd(
-        p.addr, z.data_ptr(), _ptr(h), _ptr(gate), _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(scale), _ptr(dz),
+        p.addr, z.data_ptr(), _there(h), _ptr(gate), _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(scale), _there(dz),
         _ptr(dy), _ptr(g["dx"]), _ptr(g["dh"]), _ptr(g["dgate"]), _ptr(g["dpost_weight"]), _ptr(g["dweight"]),
         _ptr(g["dbias"]), _ptr(g["dscale"]), _ptr(g["dshift"]), _ptr(ws), p.ws_bytes, _stream(p.index)))
     return g

@@ -176,6 +176,24 @@ def test_groups_without_rows_have_their_vectors_and_gradients(unlaunched, shape,
         block.norm_forward(x.detach(), h, gate=torch.ones(G, 8), scale=torch.ones(G + 1, 8), rows_per_group=rpg)
 
 
+def test_calls_without_rows_reach_the_library_as_given(L, host, monkeypatch):
+    """A tensor without elements has no address; the library, which launches nothing for it, still sees it as given."""
+    monkeypatch.setattr(block, "_stream", lambda index: 0)
+    e, v, c = torch.empty(2, 0, 8), torch.ones(2, 8), torch.ones(8)
+    z, y = block.norm_forward(e, e, gate=v, scale=v, shift=v, post_weight=c, post_norm="rms")
+    assert z.shape == y.shape == e.shape
+    assert block.norm_forward(e, e, gate=v, norm=None)[0].shape == e.shape
+    g = block.norm_backward(e, e, None, e, gate=v, scale=v)
+    assert all(torch.equal(g[k], torch.zeros(2, 8)) for k in ("dgate", "dscale", "dshift"))
+    g = block.norm_backward(e, e, e, None, gate=v, norm=None)
+    assert torch.equal(g["dgate"], torch.zeros(2, 8)) and g["dh"].shape == e.shape
+    # what is refused with rows is refused without them
+    with pytest.raises(_abi.PrismError):
+        block.norm_forward(e, gate=v)
+    with pytest.raises(_abi.PrismError):
+        block.norm_forward(e, e, post_weight=c)
+
+
 def given_outputs():
     """(name, output, call that writes it) of every output that a caller may give, in place or apart."""
     z = lambda *s: torch.zeros(*s)

@@ -19,6 +19,16 @@ def gen(seed):
     return g
 
 
+def test_groups_without_rows():
+    """Samples of no tokens on the GPU: gradients of the vectors are 0, those of all rows' vectors too."""
+    x = torch.empty(3, 0, 64, device="cuda", requires_grad=True)
+    v = {k: torch.ones(3, 64, device="cuda", requires_grad=True) for k in ("gate", "scale", "shift")}
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    z, y = block.norm(x, torch.empty(3, 0, 64, device="cuda"), weight=w, **v)
+    (z.sum() + y.sum()).backward()
+    assert x.grad.shape == x.shape and all(torch.equal(t.grad, torch.zeros_like(t)) for t in (w, *v.values()))
+
+
 # ------------------------------------------------------------------ two callers
 @pytest.mark.parametrize("widths", [(2048, 1024, 1536), (4096, 3200, 4096)])
 def test_threads_in_one_kernel_with_rows_of_other_widths(widths):
