@@ -1,4 +1,6 @@
-"""The operators around the attention on the GPU, where a fault would be lost among roundings or needs two callers."""
+"""The operators around the attention on the GPU, where a fault would be lost among roundings or needs two callers:
+column sums of whole numbers, which show a single lost or doubled row; both sides of the plan's switch between one CTA
+and several; threads in one kernel with rows of different widths; infinities beside pairs that do not turn."""
 import ctypes
 import threading
 
@@ -19,6 +21,113 @@ def gen(seed):
     return g
 
 
+def signs(g, *shape, balanced=False):
+    """-1 and 1 at random; `balanced`: as many of either in a row."""
+    if balanced:
+        return (torch.rand(*shape, generator=g, device="cuda").argsort(-1) % 2).float() * 2 - 1
+    return torch.randint(0, 2, shape, generator=g, device="cuda").float() * 2 - 1
+
+
+# ------------------------------------------------------------------ sums of whole numbers
+# Rows of -1 and 1 have the mean square 1, and the norm leaves them as they are but for the roundings of the mean square
+# (two half steps), of its reciprocal root (CUDA's bound: two units, four half steps) and of the product: seven half
+# steps.  With gradients of -1 and 1 the column sums of dy and of dz ∘ h are whole numbers below 2^24, exact in any
+# order, and those of dy ∘ N(z) and dz ∘ N(h) are off whole ones by at most R (7 + n) 2^-24, n the additions that a value
+# passes: rows a team, teams a CTA, segments and groups over 16 warps, these, and up to 8 CTAs.  n is at most 60 where
+# R is 40000, 64 at 20000 and 110 at 10007 and below: 0.16.  A lost or doubled row moves a sum by 1.
+SUM_CASES = [
+    # rows, channels, rows a group, stream, branch: the lengths at which groups are cut, run together and joined
+    (1, 64, 1, F32, F32),
+    (4999, 1100, 4999, F32, F32),
+    (6001, 320, 6001, BF16, BF16),
+    (6000, 320, 2999, F32, BF16),
+    (10007, 64, 1, F32, F32),
+    (20000, 40, 700, F32, F32),
+    (19999, 40, 700, BF16, BF16),
+    (40000, 96, 40000, BF16, BF16),
+    (39999, 96, 13333, BF16, BF16),
+    (5000, 520, 1000, BF16, BF16),
+    (2111, 264, 700, BF16, BF16),
+    (1203, 2048, 2, BF16, BF16),
+    (4097, 2048, 4097, F32, BF16),
+    (997, 4096, 997, BF16, BF16),
+    (1500, 3000, 499, F32, BF16),
+    (901, 1001, 1, BF16, BF16),
+    (1371, 1001, 97, F32, F32),
+    (611, 6000, 611, F32, F32),
+    (333, 8192, 100, BF16, BF16),
+]
+
+
+def group_sums(v, rpg):
+    R, C = v.shape
+    G = -(-R // rpg)
+    return v.new_zeros(G, C).index_add_(0, torch.arange(R, device="cuda") // rpg, v)
+
+
+@pytest.mark.parametrize("R,C,rpg,sdt,bdt", SUM_CASES)
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+@pytest.mark.parametrize("form", ["none", "plain", "normed"])
+def test_column_sums_hold_every_row_once(R, C, rpg, sdt, bdt, norm, form):
+    g = gen(R + C)
+    if norm == "layer" and C % 2:
+        pytest.skip("a row of odd width has no mean of 0")
+    z, dy, dz, h = (signs(g, R, C, balanced=i == 0) for i in range(4))
+    G = -(-R // rpg)
+    near = lambda got, want: bool(((got.double() - want).abs() <= 0.25).all())
+    kw = dict(norm=norm, eps=1e-9, rows_per_group=rpg)
+    D, A = group_sums(dy.double(), rpg), group_sums((dy * z).double(), rpg)
+    if form == "none":
+        # weight 1: dscale is A; all the vectors' gradients of the groups, then only those of all rows
+        one, zero = torch.ones(C, device="cuda"), torch.zeros(G, C, device="cuda")
+        b = block.norm_backward(z.to(sdt), None, dz.to(sdt), dy.to(bdt), weight=one, bias=one, scale=zero, **kw)
+        assert torch.equal(b["dshift"].double(), D) and near(b["dscale"], A + D)
+        assert torch.equal(b["dbias"].double(), D.sum(0)) and near(b["dweight"], A.sum(0))
+        b = block.norm_backward(z.to(sdt), None, None, dy.to(bdt), weight=one, bias=one, **kw)
+        assert torch.equal(b["dbias"].double(), D.sum(0)) and near(b["dweight"], A.sum(0))
+        return
+    # weight 0: nothing of y reaches dz', which stays dz; gates of 1 and 2
+    w = torch.zeros(C, device="cuda")
+    gate = 1.0 + torch.randint(0, 2, (G, C), generator=g, device="cuda")
+    B = group_sums((dz * h).double(), rpg)
+    post = dict(post_norm="rms", post_weight=torch.ones(C, device="cuda")) if form == "normed" else {}
+    b = block.norm_backward(z.to(sdt), h.to(bdt), dz.to(sdt), dy.to(bdt), weight=w, bias=w, gate=gate,
+                            scale=torch.zeros(G, C, device="cuda"), **kw, **post)
+    assert torch.equal(b["dshift"].double(), D) and torch.equal(b["dbias"].double(), D.sum(0))
+    assert near(b["dweight"], A.sum(0)) and near(b["dgate"], B)
+    if form == "normed":
+        # a row counts once or twice by its gate, and so does the bound
+        assert bool(((b["dpost_weight"].double() - (gate.double() * B).sum(0)).abs() <= 0.5).all())
+    else:
+        assert torch.equal(b["dgate"].double(), B)
+
+
+# Quarter turns: cosines and sines of 0, 1 and -1, whole numbers again.  The bound is as above with R = tokens x heads; n
+# counts a group of lanes' heads, the 16 or 32 groups of a CTA, the CTAs over 16 warps and these.  It is largest for
+# 12345 x 3 heads: 4 + 32 + 28 + 16 = 80, 0.19.
+@pytest.mark.parametrize("N,grid,hq,hk,d,dt,pairs", [
+    (5000, (8, 25, 25), 2, 3, 128, F32, "half"), (5001, (8, 25, 25), 3, 2, 128, BF16, "interleaved"),
+    (2999, (2, 30, 50), 0, 5, 64, F32, "half"), (117, (1, 9, 13), 5, 1, 64, BF16, "half"),
+    (12345, (5, 47, 53), 3, 0, 64, BF16, "interleaved"), (1, (1, 1, 1), 1, 1, 64, F32, "interleaved")])
+def test_rotation_weight_sums_hold_every_head_once(N, grid, hq, hk, d, dt, pairs):
+    g = gen(N)
+    axes = (d // 8, d // 8, d // 8)                 # a quarter of the pairs does not turn
+    rows = sum(n * p for n, p in zip(grid, axes))
+    turn = torch.randint(0, 4, (rows,), generator=g, device="cuda")
+    table = torch.tensor([[1, 0], [0, 1], [-1, 0], [0, -1]], dtype=F32, device="cuda")[turn]
+    x = [signs(g, N, h, d) if h else None for h in (hq, hk)]
+    dr = [signs(g, N, h, d) if h else None for h in (hq, hk)]
+    w = [torch.ones(d, device="cuda") if h else None for h in (hq, hk)]
+    to = lambda t: None if t is None else t.to(dt)
+    got = block.rotate_backward(*map(to, x), *map(to, dr), table, grid=grid, axes=axes, q_weight=w[0], k_weight=w[1],
+                                eps=1e-9, pairs=pairs)
+    cos, sin = bf.angles(table, grid, axes, N, d)
+    for a, b, name in ((x[0], dr[0], "dq_weight"), (x[1], dr[1], "dk_weight")):
+        if a is not None:
+            want = (bf.rotate(b.double(), None, cos, -sin, pairs, 0) * a.double()).sum((0, 1))
+            assert bool(((got[name].double() - want).abs() <= 0.25).all()), name
+
+
 def test_groups_without_rows():
     """Samples of no tokens on the GPU: gradients of the vectors are 0, those of all rows' vectors too."""
     x = torch.empty(3, 0, 64, device="cuda", requires_grad=True)
@@ -27,6 +136,24 @@ def test_groups_without_rows():
     z, y = block.norm(x, torch.empty(3, 0, 64, device="cuda"), weight=w, **v)
     (z.sum() + y.sum()).backward()
     assert x.grad.shape == x.shape and all(torch.equal(t.grad, torch.zeros_like(t)) for t in (w, *v.values()))
+
+
+# ------------------------------------------------------------------ expert plan
+@pytest.mark.parametrize("R,k", [(2047, 1), (2048, 1), (2049, 1), (1024, 2), (683, 3), (128, 16), (129, 16), (1025, 2)])
+@pytest.mark.parametrize("E,align,dropped", [(7, 1, 0.0), (300, 8, 0.1), (1024, 3, 0.0)])
+def test_expert_plan_where_one_cta_ends(R, k, E, align, dropped):
+    """2048 slots are sorted by one CTA, 2049 by two launches, whose third CTA has a single slot."""
+    g = gen(R * k + E)
+    ids = torch.randint(0, E, (R, k), generator=g, device="cuda")
+    ids[torch.rand(R, k, generator=g, device="cuda") < dropped] = -1
+    plan = block.expert_plan(ids, E, align=align)
+    want = bf.experts(ids.cpu(), E, align, plan.rows_sorted)
+    for got, w in zip((plan.counts, plan.offsets, plan.pos, plan.src), want):
+        assert torch.equal(got.cpu(), w)
+    x = torch.randn(R, 24, generator=g, device="cuda")
+    src = plan.src.long()
+    xs = block.expert_dispatch(x, plan)
+    assert torch.equal(xs, torch.where((src >= 0)[:, None], x[src.clamp(min=0) // k], torch.zeros((), device="cuda")))
 
 
 # ------------------------------------------------------------------ two callers
