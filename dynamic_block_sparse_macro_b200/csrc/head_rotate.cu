@@ -446,16 +446,13 @@ static unsigned ctas_of(const Args& a, int sides, int per_sm) {
     return (unsigned)(want < most ? want : most);
 }
 
-template <typename T, int D, bool HALF, bool BWD> static prism_status_t launch_one(const Args& a, dim3 grid, cudaStream_t s) {
+template <typename T, int D, bool HALF, bool BWD> static void launch_one(const Args& a, dim3 grid, cudaStream_t s) {
     auto kernel = a.turn < D / 2 ? &k_head_rotate<T, D, HALF, BWD, true> : &k_head_rotate<T, D, HALF, BWD, false>;
     constexpr int bytes = steps_ahead(sizeof(T), HALF, BWD) * 2 * heads_at_once(sizeof(T), HALF, BWD) * 8 * (int)sizeof(T) * 256;
-    if (bytes > 32 << 10 &&                       // with the static part, more than the 48 KB that need no leave
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return PRISM_ERR_CUDA;
+    static_assert(bytes <= 36 << 10, "with the static part, within the 48 KB that need no leave");
     kernel<<<grid, 256, bytes, s>>>(a);
-    return PRISM_OK;
 }
-template <bool BWD> static prism_status_t launch(const prism_rotate_t* p, const Args& a, dim3 grid, cudaStream_t s) {
+template <bool BWD> static void launch(const prism_rotate_t* p, const Args& a, dim3 grid, cudaStream_t s) {
 #define PRISM_ROT_D(T)                                                                                                 \
     do {                                                                                                               \
         if (p->head_dim == 128)                                                                                        \
@@ -522,16 +519,15 @@ static prism_status_t rotate(const prism_rotate_t* p, const void* Q, const void*
     const unsigned ctas = ctas_of(a, sides, ctas_sm(p->dtype == PRISM_BF16 ? 2 : 4, bwd));
     const dim3 grid(ctas, sides);
     if (!bwd) {
-        const prism_status_t r = launch<false>(p, a, grid, stream);
-        return r == PRISM_OK ? launch_status(1) : r;
+        launch<false>(p, a, grid, stream);
+        return launch_status(1);
     }
     const bool dw = dwq || dwk;
     if (dw) {
         if (!ws || ws_bytes < (size_t)kMaxCtas * p->head_dim * sizeof(float)) return PRISM_ERR_WORKSPACE;
         a.part = (float*)ws;
     }
-    const prism_status_t r = launch<true>(p, a, grid, stream);
-    if (r != PRISM_OK) return r;
+    launch<true>(p, a, grid, stream);
     if (dw) {
         if (!launched() ||
             !launch_after(k_head_rotate_join, dim3(p->head_dim / 32, sides), dim3(32, 16), 1, stream, (const float*)a.part,
