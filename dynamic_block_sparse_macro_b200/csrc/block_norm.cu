@@ -177,12 +177,6 @@ static prism_status_t check(const prism_block_norm_t* n) {
     return PRISM_OK;
 }
 
-// the row stride in elements (0: dense); false when rows would overlap
-static bool ld_of(int64_t ld, int C, int64_t* out) {
-    *out = ld == 0 ? C : ld;
-    return *out >= C;
-}
-
 // channels an access may take: all strides in use and the width are multiples of it, and all addresses of its bytes
 static int unit_of(int wide, int C, std::initializer_list<int64_t> lds, std::initializer_list<const void*> ptrs) {
     Bits n, p;
@@ -191,7 +185,6 @@ static int unit_of(int wide, int C, std::initializer_list<int64_t> lds, std::ini
     for (const void* q : ptrs) p << q;
     return n.multiple_of(wide) && p.multiple_of(16) ? wide : n.multiple_of(2) && p.multiple_of(8) ? 2 : 1;
 }
-static int esize(int dtype) { return dtype == PRISM_BF16 ? 2 : 4; }
 
 }  // namespace bn
 }  // namespace prism

@@ -458,7 +458,6 @@ static int unit_bytes(int esz, int64_t C, std::initializer_list<int64_t> lds, st
     for (const void* p : ptrs) m << p;
     return m.multiple_of(16) ? 16 : m.multiple_of(4) ? 4 : 2;
 }
-static int esize(int dtype) { return dtype == PRISM_BF16 ? 2 : 4; }
 
 static prism_status_t move_args(const prism_experts_t* e, int dtype, int64_t channels, const int32_t* pos, MoveArgs* a) {
     const prism_status_t st = check(e);
@@ -470,10 +469,6 @@ static prism_status_t move_args(const prism_experts_t* e, int dtype, int64_t cha
     a->R = e->rows; a->cap = capacity(e); a->C = (int)channels; a->k = e->top_k; a->E = e->experts;
     a->pos = pos;
     return PRISM_OK;
-}
-static bool ld_of(int64_t ld, int64_t C, int64_t* out) {
-    *out = ld == 0 ? C : ld;
-    return *out >= C;
 }
 
 #define PRISM_EX_BY_UNIT(KERNEL, B, GRID, S, A)                                        \

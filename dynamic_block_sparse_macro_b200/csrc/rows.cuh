@@ -21,6 +21,13 @@ struct Bits {
 inline bool on(const void* p, int b) { return p != nullptr && (uintptr_t)p % b == 0; }
 inline bool opt_on(const void* p, int b) { return (uintptr_t)p % b == 0; }
 
+inline int esize(int dtype) { return dtype == PRISM_BF16 ? 2 : 4; }
+// the row stride in elements (0: dense); false when rows would overlap
+inline bool ld_of(int64_t ld, int64_t C, int64_t* out) {
+    *out = ld == 0 ? C : ld;
+    return *out >= C;
+}
+
 // Whether the runtime took the call that has just been made (r: its own answer).  A refusal is this call's to report:
 // nothing further is launched, and it is not left behind for the next call's check.
 inline bool taken(cudaError_t r) { return r == cudaSuccess || (cudaGetLastError(), false); }
