@@ -19,13 +19,15 @@
 // Bound by HBM: every row is read and written once.  A row's threads hold eight channels each, a few lanes, a warp or a
 // CTA of up to 1024 threads, and keep the vectors of the row's group in registers from row to row.  What is past the
 // row's end enters no sum.  Of what decides the speed:
-//   - no spills: the f32 / bf16 forward at 131072 x 2048 took 705 us with 88 bytes of them and takes 501 without (498
+//   - few spills or none: the f32 / bf16 forward at 131072 x 2048 took 705 us with 88 bytes of them and takes 501 without (498
 //     at the measured copy rate); with more CTAs an SM (64 registers, 112 bytes) 747;
 //   - fp32 pairs in one instruction: the backward of 61440 x 2048 339 -> 248 us, rows copied three ahead included; with
 //     one barrier a row less 243 (233);
-//   - the widest teams (more than 512 threads, backwards 384) have an SM to themselves and leave it idle at each of a
-//     row's barriers: 8191 x 5120 with two rms norms 98 us (78), 13269 x 8192 276 (202).  Clusters of CTAs of 256 threads
-//     in their place wait longer for one another: 13269 x 4096 149 us instead of 128, with the cluster's barrier 229.
+//   - the widest teams have an SM to themselves and leave it idle at each of a row's barriers: backwards more than 384
+//     threads (f32 stream and branch: 320), forwards with a branch more than 512 (narrow accesses: 384), without one more
+//     than 768 (narrow accesses as with a branch); see fwd_ctas and bwd_ctas.  8191 x 5120 with two rms norms 98 us (78),
+//     13269 x 8192 276 (202).  Clusters of CTAs of 256 threads in their place wait longer for one another: 13269 x 4096
+//     149 us instead of 128, with the cluster's barrier 229.
 //   - rows of odd width move element by element: 40000 x 1001 bf16 218 us backwards, x 1000 93.
 #pragma once
 
@@ -142,7 +144,7 @@ template <typename T, int E> __device__ __forceinline__ void put_units(T* row, c
     }
 }
 
-// D > 0: D rows ahead through shared memory (teams that have an SM to themselves), else one through registers.
+// D > 0: D rows ahead through shared memory (teams of more than 256 threads), else one through registers.
 template <typename TX, typename TH, int E, int MAXT, bool HAS_H, int CTAS, int D>
 __global__ void __launch_bounds__(MAXT == 32 ? 256 : MAXT, CTAS) k_block_norm_fwd(const FwdArgs a) {
     constexpr int U = 8 / E;
