@@ -467,7 +467,7 @@ def rotation_table(grid, axes, base=10000.0, device="cuda", positions=None):
     parts = []
     for a, (length, pairs) in enumerate(zip(grid, axes)):
         p = torch.arange(length, dtype=torch.float64) if positions is None else torch.as_tensor(
-            positions[a], dtype=torch.float64)
+            positions[a], dtype=torch.float64, device="cpu")
         _need(p.shape == (length,), f"axis {a} has {length} places, not {tuple(p.shape)}")
         angle = p[:, None] * base ** (-torch.arange(pairs, dtype=torch.float64) / max(1, pairs))
         parts.append(torch.stack((angle.cos(), angle.sin()), -1).reshape(-1, 2))

@@ -249,3 +249,10 @@ def test_rotation_backward_of_rows_of_zeros_with_the_smallest_eps(pairs):
     terms = dr.double().abs().amax() * 2 * r
     # two products and a sum, the reciprocal root (four half steps), a product with it and one with the weight: 9
     assert bool(((got.double() - want).abs() <= 9 * bf.U * terms).all())
+
+
+def test_rotation_table_of_places_on_the_gpu():
+    places = [torch.tensor(p) for p in ([0.0, 5.0], [1.0, 2.0, 3.0], [0.0, 0.5])]
+    kw = dict(grid=(2, 3, 2), axes=(2, 1, 3))
+    assert torch.equal(block.rotation_table(positions=[p.cuda() for p in places], **kw),
+                       block.rotation_table(positions=places, **kw))
