@@ -280,7 +280,7 @@ def prism_attention(Q, K, V, hhat, mod: PrismSparseAttention, rotation: dict | N
     rotation: arguments of ``block.rotate`` (``table``, ``axes``, and as wanted
     ``q_weight``, ``k_weight``, ``norm``, ``eps``, ``pairs``) for the norm and
     the rotation of Q and K on the layer's grid, which the attention then reads;
-    the gradients go back through them.
+    the gradients go back through them (and cannot be captured into a graph).
     """
     if rotation is not None:
         from . import block
