@@ -302,8 +302,9 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
 
     x [..., C] is the residual stream, h [..., C] the block's output (None: z is x); gate, scale and shift are
     float32 [groups, C], one row for each ``rows_per_group`` rows (default: x's last-but-one dimension where it has
-    three or more, else all rows; without rows any number of groups); weight, bias and post_weight float32 [C].  ``norm=None`` gives no y.  y has
-    ``out_dtype`` (default: h's type, else x's).  ``z`` and ``y`` may be given as outputs; z may be x itself.
+    three or more, else all rows; without rows any number of groups); weight, bias and post_weight float32 [C].
+    ``norm=None`` gives no y.  y has ``out_dtype`` (default: h's type, else x's).  ``z`` and ``y`` may be given as
+    outputs; z may be x itself.
     """
     eps, res_scale, rows_per_group = _real(eps, "eps"), _real(res_scale, "res_scale"), _group_rows(rows_per_group)
     key = ("norm", x.shape, x.stride(), x.dtype, x.device, _sig(h), _sig(gate), _sig(post_weight), _sig(weight), _sig(bias),
