@@ -55,7 +55,8 @@ def _real(v, what):
     """A number that a kept call holds: its value now, where it is a tensor of one element."""
     if type(v) is float:
         return v
-    _need(not (isinstance(v, torch.Tensor) and v.requires_grad), f"{what} is a number and gets no gradient")
+    if isinstance(v, torch.Tensor) and v.requires_grad:
+        raise ValueError(f"{what} is a number and gets no gradient")
     return float(v)
 
 
@@ -70,7 +71,8 @@ def _group_rows(v):
 
 
 def _whole(values):
-    _need(len(values) == 3, "grid and axes have three entries: (T, H, W)")
+    if len(values) != 3:
+        raise ValueError("grid and axes have three entries: (T, H, W)")
     a, b, c = values
     return (a, b, c) if type(a) is type(b) is type(c) is int else (index(a), index(b), index(c))
 
@@ -197,15 +199,14 @@ def _itself(a, b):
 
 
 def _writable(out, what):
-    _need(not (out.requires_grad and torch.is_grad_enabled()),
-          f"{what} requires grad and is written without autograd's knowledge: use torch.no_grad()")
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires grad and is written without autograd's knowledge: use torch.no_grad()")
 
 
-def _written(*outs):
-    """Tells autograd that given outputs have new values: a backward that needs the old ones then raises."""
-    for t in outs:
-        if t is not None and not t.is_inference():           # inference tensors have no version
-            increment_version(t)
+def _written(t):
+    """Tells autograd that a given output has new values: a backward that needs the old ones then raises."""
+    if t is not None and not t.is_inference():               # inference tensors have no version
+        increment_version(t)
 
 
 def _check_out(out, what, allowed, *others):
@@ -333,7 +334,7 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
             return norm_forward(x, h, gate=gate, post_weight=post_weight, weight=weight, bias=bias, scale=scale,
                                 shift=shift, norm=norm, post_norm=post_norm, eps=eps, res_scale=res_scale,
                                 rows_per_group=rows_per_group, out_dtype=out_dtype, z=z, y=y)
-    given = (z, y)
+    given = () if z is None and y is None else (z, y)
     if z is not None:
         # h may be x, in place too: a row's h is read before its z is written
         _check_out(z, "z", x, None if _itself(h, x) else h, gate, post_weight, weight, bias, scale, shift)
@@ -346,7 +347,8 @@ def norm_forward(x, h=None, *, gate=None, post_weight=None, weight=None, bias=No
     _check("prism_block_norm_fwd", _abi.lib().prism_block_norm_fwd(
         p.addr, x.data_ptr(), _there(h), _ptr(gate), _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(scale),
         _ptr(shift), _ptr(z), _ptr(y), _stream(p.index)))
-    _written(*given)
+    for t in given:
+        _written(t)
     return (x if h is None else z), y
 
 
@@ -587,7 +589,8 @@ def rotate_forward(Q, K, table, *, grid, axes, q_weight=None, k_weight=None, nor
         p.addr, _ptr(Q), _ptr(K), _ptr(q_weight), _ptr(k_weight), table.data_ptr(), _ptr(oq), _ptr(ok),
         _stream(p.index)))
     if out is not None:
-        _written(oq, ok)
+        _written(oq)
+        _written(ok)
     return oq, ok
 
 
@@ -836,7 +839,8 @@ def expert_combine(ys, plan, weights=None, *, add=None, out=None):
                                            _stream(p.index))
     if code:
         raise _abi.PrismError("prism_expert_combine", code)
-    _written(given)
+    if given is not None:
+        _written(given)
     return out
 
 
